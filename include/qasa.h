@@ -82,8 +82,9 @@ typedef enum {
 #define QASA_DEVERR_SEQ_LEN   0x2  /* seq_len < 0 or beyond max_pages_per_seq*page_size: clamped */
 #define QASA_DEVERR_BUDGET    0x4  /* kept pages would exceed max_budget: clamped */
 #define QASA_DEVERR_TIMEOUT   0x8  /* a bounded wait in a pipelined kernel gave up */
-#define QASA_DEVERR_APPEND    0x10 /* append_lens[b] outside [0, max_new_tokens]: clamped */
+#define QASA_DEVERR_APPEND    0x10 /* append_lens[b] (q_lens[b]) outside [0, max_new_tokens (max_q_tokens)]: clamped */
 #define QASA_DEVERR_SELECTED  0x20 /* a selected id outside [0, N_b): page skipped */
+#define QASA_DEVERR_POSITION  0x40 /* a token's position is beyond the rotation table: token skipped */
 
 typedef struct {
     void *k_pool;            /* [num_phys_pages][num_kv_heads][page_size][head_dim] */
@@ -137,6 +138,60 @@ qasa_status qasa_kv_append(const qasa_kv_cache *cache, const int32_t *block_tabl
                            const int32_t *append_lens, const void *k_new, const void *v_new,
                            int32_t batch, int32_t max_new_tokens, int32_t *device_status,
                            cudaStream_t stream);
+
+/*
+ * Append with the position rotation applied on the way: raw queries, keys and
+ * values of the new tokens in, rotated keys and the values in their pages (boxes
+ * and E4M3 scales kept current as by qasa_kv_append), rotated queries out.  One
+ * launch takes the place of a rotation of q, a rotation of k and qasa_kv_append.
+ *
+ * The token at position pos = seq_lens[b] + t turns the channel pairs (a, b) of
+ * every head by the angles of row `pos` of the table:
+ *     y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin          (fp32)
+ * Pair i (i < rot_dim / 2) is channels (i, i + rot_dim / 2), or with
+ * `interleaved` channels (2i, 2i + 1); channels >= rot_dim stay as they are.  A
+ * rotated value is rounded once: to the cache dtype (f16 for the queries of an
+ * E4M3 cache), or to the page's E4M3 code.  The box holds the min / max of the
+ * keys as stored.
+ */
+typedef struct {
+    const float *table;        /* device, [max_positions][2][rot_dim / 2]: a row of cosines, a row of sines */
+    int32_t max_positions;
+    int32_t rot_dim;           /* a multiple of 16, at most head_dim */
+    int32_t interleaved;       /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+} qasa_rotation;
+
+/* Rows of new tokens, [batch][tokens][heads][head_dim]: a token's heads are
+ * contiguous, tokens and sequences at any distance (in elements, not negative, a
+ * multiple of 16 bytes), so that q, k and v may be parts of one projection's
+ * output.  A stride that no address uses (one token, one sequence) is not
+ * looked at. */
+typedef struct {
+    const void *data;
+    int64_t batch_stride;
+    int64_t token_stride;
+} qasa_token_rows;
+
+/*
+ *   rotation       as above; with a table of at least max_pages_per_seq * page_size
+ *                  positions no cached token can lie beyond it
+ *   q              num_q_heads heads per token, or NULL: nothing to rotate but k
+ *   q_out          [batch][max_new_tokens][num_q_heads][head_dim] out (NULL with q
+ *                  NULL); may be q's own memory where q has exactly this layout,
+ *                  and must not overlap any other argument.  Rows of tokens at or
+ *                  past the sequence's count are left as they were.
+ *   other arguments as in qasa_kv_append
+ * A token whose position the table does not have is skipped, q included, and sets
+ * QASA_DEVERR_POSITION.  A token that has no page (beyond the block table, or a
+ * bad entry) is reported as by qasa_kv_append; its query is rotated all the same.
+ */
+qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotation *rotation,
+                                   const int32_t *block_table, int32_t max_pages_per_seq,
+                                   const int32_t *seq_lens, const int32_t *append_lens,
+                                   const qasa_token_rows *q, int32_t num_q_heads, void *q_out,
+                                   const qasa_token_rows *k_new, const qasa_token_rows *v_new,
+                                   int32_t batch, int32_t max_new_tokens, int32_t *device_status,
+                                   cudaStream_t stream);
 
 /*
  * Rebuild the page boxes of whole sequences from the keys already in k_pool:
@@ -241,6 +296,41 @@ qasa_status qasa_dense_decode_attention(const qasa_kv_cache *cache, const void *
                                         float scale, void *out, void *workspace,
                                         size_t workspace_bytes, int32_t batch,
                                         int32_t *device_status, cudaStream_t stream);
+
+/*
+ * Attention of the newest tokens of every sequence over the paged cache, with a
+ * sliding window and a few first tokens that stay visible (sinks): decode steps,
+ * the verification of drafted tokens and prompts (in one piece or in chunks) of
+ * windowed layers, and with window = INT32_MAX of layers that see everything.
+ *
+ * Sequence b has seq_lens[b] tokens, whose keys and values are in the cache; its
+ * queries are those of its newest n_b tokens, n_b = q_lens[b] if q_lens is
+ * non-NULL, else max_q_tokens.  Query t is at position i = seq_lens[b] - n_b + t
+ * and sees the tokens j <= i with j < sink_tokens or j > i - window:
+ *     out = sum_j softmax_j(scale * q.k_j) v_j
+ * fp32 statistics and sums; scale <= 0 selects 1/sqrt(d).  A query that sees
+ * nothing (a position below 0, pages that are all bad) gets zeros.
+ *   q, out         [batch][max_q_tokens][num_q_heads][head_dim]; rows of out at or
+ *                  past n_b are left as they were
+ *   window         >= 1, the query's own token included
+ *   sink_tokens    >= 0
+ *   workspace      device memory of qasa_window_workspace_size bytes, 16-byte
+ *                  aligned (scratch, no initialisation; NULL where that is 0)
+ * Any group size 1..8, max_q_tokens up to 65536.  Pages that hold no token that
+ * some query of the sequence sees are not read, and neither are their block-table
+ * entries: a rolling cache may have given them back.  Keys and values of tokens
+ * that some query of the call sees must be finite; slots that none sees may hold
+ * anything.
+ */
+size_t qasa_window_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
+                                  int32_t max_q_tokens, int32_t max_pages_per_seq, int32_t window,
+                                  int32_t sink_tokens);
+qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
+                                  int32_t max_q_tokens, const int32_t *q_lens,
+                                  const int32_t *block_table, int32_t max_pages_per_seq,
+                                  const int32_t *seq_lens, int32_t window, int32_t sink_tokens,
+                                  float scale, void *out, void *workspace, size_t workspace_bytes,
+                                  int32_t batch, int32_t *device_status, cudaStream_t stream);
 
 /* Bytes of the fixed device buffer that qasa_sparse_decode_attention_noalloc
  * uses in place of a workspace (held by every device that loads the library). */

@@ -30,6 +30,7 @@ DEVERR = {
     0x8: "bounded wait timed out",
     0x10: "append length out of range",
     0x20: "selected id out of range",
+    0x40: "position beyond the rotation table",
 }
 
 
@@ -39,6 +40,15 @@ class _Cache(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("page_scales", ctypes.c_void_p)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class _TokenRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -63,6 +73,14 @@ _lib.qasa_dense_decode_attention.restype = _I
 _lib.qasa_sparse_decode_attention_noalloc.argtypes = [_C, _P, _I, _P, _I, _P, _P, _I, ctypes.c_float,
                                                       _P, _P, _P, _I, _P, _P]
 _lib.qasa_sparse_decode_attention_noalloc.restype = _I
+_R = ctypes.POINTER(_TokenRows)
+_lib.qasa_kv_append_rotated.argtypes = [_C, ctypes.POINTER(_Rotation), _P, _I, _P, _P, _R, _I, _P, _R, _R, _I, _I, _P, _P]
+_lib.qasa_kv_append_rotated.restype = _I
+_lib.qasa_window_workspace_size.argtypes = [_I, _I, _C, _I, _I, _I, _I]
+_lib.qasa_window_workspace_size.restype = ctypes.c_size_t
+_lib.qasa_window_attention.argtypes = [_C, _P, _I, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t,
+                                       _I, _P, _P]
+_lib.qasa_window_attention.restype = _I
 _lib.qasa_rebuild_page_bounds.argtypes = [_C, _P, _I, _P, _I, _P, _P]
 _lib.qasa_rebuild_page_bounds.restype = _I
 _lib.qasa_page_attention_mass.argtypes = [_C, _P, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _P]
@@ -88,7 +106,8 @@ EXPORTED = ("qasa_kv_append", "qasa_decode_workspace_size", "qasa_select_pages",
             "qasa_dense_decode_attention", "qasa_sparse_decode_attention_noalloc",
             "qasa_rebuild_page_bounds", "qasa_page_attention_mass", "qasa_page_hit_rate",
             "qasa_host_decode_workspace_size", "qasa_sparse_decode_attention_host",
-            "qasa_host_call_is_direct", "qasa_status_string", "qasa_version",
+            "qasa_host_call_is_direct", "qasa_kv_append_rotated", "qasa_window_workspace_size",
+            "qasa_window_attention", "qasa_status_string", "qasa_version",
             "qasa_debug_trace_bytes", "qasa_debug_trace")
 
 # trace buffer layout (include/qasa.h)
@@ -221,6 +240,164 @@ def kv_append(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Te
                                _ptr(seq_lens), _ptr(append_lens), _ptr(k_new), _ptr(v_new), B, T,
                                _ptr(status), _stream(stream))
     _check(code, "qasa_kv_append")
+
+
+def _checked(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, device: torch.device):
+    """Address of a contiguous tensor of this type, shape and device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
+    return t.data_ptr()
+
+
+def _checked_status(status: Optional[torch.Tensor], device: torch.device):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor on %s" % device)
+    return status.data_ptr()
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, head_dim: int, device: torch.device) -> _TokenRows:
+    if t.dim() != 4 or t.dtype != dtype or t.device != device or t.shape[3] != head_dim:
+        raise ValueError("%s must be a %s tensor [batch, tokens, heads, %d] on %s" % (name, dtype, head_dim, device))
+    sb, st, sh, sc = t.stride()
+    if (sc != 1 or (sh != head_dim and t.shape[2] > 1)) and t.numel():
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    return _TokenRows(t.data_ptr(), sb, st)
+
+
+class _OnDevice:
+    """The stream of a call on `device`: the one given, else the device's current
+    one, with the device made current around the call where another one is."""
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if device.type != "cuda":
+            raise ValueError("the cache must be on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError("stream and cache are on different devices")
+        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def rotation_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines of the angles pos * base^(-2 i / rot_dim), [max_positions, 2, rot_dim / 2]
+    float32, computed in 64 bits (a far position's angle has few 32-bit digits left).  Any other
+    table of this layout serves too (scaled or interpolated frequencies)."""
+    freq = torch.pow(torch.tensor(float(base), dtype=torch.float64), -torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    angle = torch.arange(max_positions, dtype=torch.float64)[:, None] * freq
+    return torch.stack((angle.cos(), angle.sin()), 1).to(torch.float32).contiguous().to(device)
+
+
+def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Tensor, k_new: torch.Tensor,
+                      v_new: torch.Tensor, table: torch.Tensor, q: Optional[torch.Tensor] = None,
+                      q_out: Optional[torch.Tensor] = None, append_lens: Optional[torch.Tensor] = None,
+                      interleaved: bool = False, status: Optional[torch.Tensor] = None,
+                      stream=None) -> Optional[torch.Tensor]:
+    """kv_append with the position rotation applied on the way: k_new [B, T, Hkv, d] is rotated by the
+    table's angles of its positions before it is stored, q [B, T, Hq, d] (optional) is rotated into
+    q_out [B, T, Hq, d] (contiguous, allocated where not given, returned).  k_new, v_new and q may be
+    parts of one tensor: any batch and token stride that is a multiple of 16 bytes.  table: as made by
+    rotation_table, whose last dimension says how many channels turn; interleaved: neighbouring
+    channels are the pairs (else channels rot_dim / 2 apart)."""
+    dev = cache.k_pool.device
+    value = torch.float16 if cache.is_fp8 else cache.dtype
+    d = cache.head_dim
+    kr = _token_rows(k_new, "k_new", value, d, dev)
+    vr = _token_rows(v_new, "v_new", value, d, dev)
+    B, T, H = k_new.shape[:3]
+    if H != cache.num_kv_heads or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [batch, tokens, num_kv_heads, head_dim]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages_per_seq]")
+    maxp = block_table.shape[1]
+    if table.dim() != 3 or table.shape[1] != 2:
+        raise ValueError("table must be [max_positions, 2, rot_dim / 2]")
+    rot = _Rotation(_checked(table, "table", torch.float32, table.shape, dev), table.shape[0], 2 * table.shape[2],
+                    1 if interleaved else 0)
+    qr = None
+    hq = 0
+    if q is not None:
+        qr = _token_rows(q, "q", value, d, dev)
+        hq = q.shape[2]
+        if q.shape[0] != B or q.shape[1] != T:
+            raise ValueError("q must have the batch and tokens of k_new")
+        if q_out is None:
+            q_out = torch.empty((B, T, hq, d), dtype=value, device=dev)
+        qr = ctypes.byref(qr)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _OnDevice(dev, stream) as on:
+        code = _lib.qasa_kv_append_rotated(
+            cache.c_ref, ctypes.byref(rot), _checked(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
+            _checked(seq_lens, "seq_lens", torch.int32, (B,), dev),
+            _checked(append_lens, "append_lens", torch.int32, (B,), dev), qr, hq,
+            _checked(q_out, "q_out", value, (B, T, hq, d), dev), ctypes.byref(kr), ctypes.byref(vr), B, T,
+            _checked_status(status, dev), on)
+    _check(code, "qasa_kv_append_rotated")
+    return q_out
+
+
+NO_WINDOW = 0x7FFFFFFF      # a window that every token is in
+
+
+def alloc_window_workspace(cache: PagedKVCache, batch: int, num_q_heads: int, max_q_tokens: int,
+                           max_pages_per_seq: int, window: Optional[int] = None, sink_tokens: int = 0) -> torch.Tensor:
+    """Workspace of window_attention calls of up to this shape with this window."""
+    n = int(_lib.qasa_window_workspace_size(batch, num_q_heads, cache.c_ref, max_q_tokens, max_pages_per_seq,
+                                            NO_WINDOW if window is None else int(window), sink_tokens))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_pool.device)
+
+
+def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     window: Optional[int] = None, sink_tokens: int = 0, q_lens: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of the newest tokens of every sequence: q [B, T, Hq, d] (or [B, Hq, d], one token each)
+    holds the queries of the last q_lens[b] (default T) of its seq_lens[b] tokens, each of which sees
+    itself and what came before within `window` tokens (None: everything) and the first `sink_tokens`.
+    Rows at or past q_lens[b] of `out` are left as they were (unset where it is allocated here)."""
+    dev = cache.k_pool.device
+    value = torch.float16 if cache.is_fp8 else cache.dtype
+    shape = q.shape
+    if len(shape) == 4:
+        B, T, hq, d = shape
+    elif len(shape) == 3:
+        (B, hq, d), T = shape, 1
+    else:
+        raise ValueError("q must be [batch, tokens, heads, head_dim] or [batch, heads, head_dim]")
+    if d != cache.head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages_per_seq]")
+    maxp = block_table.shape[1]
+    w = NO_WINDOW if window is None else int(window)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = alloc_window_workspace(cache, B, hq, T, maxp, window, sink_tokens)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous memory on %s" % dev)
+    with _OnDevice(dev, stream) as on:
+        code = _lib.qasa_window_attention(
+            cache.c_ref, _checked(q, "q", value, shape, dev), hq, T, _checked(q_lens, "q_lens", torch.int32, (B,), dev),
+            _checked(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
+            _checked(seq_lens, "seq_lens", torch.int32, (B,), dev), w, int(sink_tokens), scale or 0.0,
+            _checked(out, "out", value, shape, dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            B, _checked_status(status, dev), on)
+    _check(code, "qasa_window_attention")
+    return out
 
 
 def rebuild_page_bounds(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,

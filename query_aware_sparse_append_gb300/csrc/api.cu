@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kMaxPagesPerSeq = 16384;
 constexpr int kMaxBatch = 8192;
+constexpr int kMaxQueryTokens = 65536;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr int kAttnUnitWeight = 4;
 
@@ -385,6 +386,23 @@ qasa_status run_attention(const qasa_kv_cache *cache, const void *q, int num_q_h
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 
+// The most 16-token tiles that one query tile of a call can see.
+long long most_visible_tiles(int max_pages, int P, int T, int window, int sinks) {
+    const long long all = (long long)max_pages * P / 16;
+    const long long body = ((long long)window + T + 14) / 16 + 1;
+    const long long seen = body + ((long long)sinks + 15) / 16;
+    return seen < all ? seen : all;
+}
+
+// CTAs per unit of the few-rows kernel: as many as fill the SMs with four CTAs
+// each, while every warp has two tiles left.
+int window_cluster(long long units, long long tiles) {
+    const int sms = sm_count() > 0 ? sm_count() : 152;
+    int c = 1;
+    while (c < 8 && units * c < 4LL * sms && tiles >= 4LL * 2 * 2 * c) c *= 2;
+    return c;
+}
+
 }  // namespace
 
 extern "C" {
@@ -420,6 +438,132 @@ qasa_status qasa_kv_append(const qasa_kv_cache *cache, const int32_t *block_tabl
     p.T = max_new_tokens;
     p.scales = cache->page_scales;
     cudaError_t e = launch_append(cache->dtype, cache->head_dim, p, batch, stream);
+    return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotation *rotation,
+                                   const int32_t *block_table, int32_t max_pages_per_seq,
+                                   const int32_t *seq_lens, const int32_t *append_lens,
+                                   const qasa_token_rows *q, int32_t num_q_heads, void *q_out,
+                                   const qasa_token_rows *k_new, const qasa_token_rows *v_new,
+                                   int32_t batch, int32_t max_new_tokens, int32_t *device_status,
+                                   cudaStream_t stream) {
+    qasa_status st = check_cache(cache);
+    if (st != QASA_OK) return st;
+    if (!rotation) return QASA_ERR_NULL;
+    if (rotation->rot_dim < 16 || rotation->rot_dim % 16 || rotation->rot_dim > cache->head_dim ||
+        rotation->max_positions < 1 || (rotation->interleaved != 0 && rotation->interleaved != 1))
+        return QASA_ERR_SHAPE;
+    if (batch == 0 || max_new_tokens == 0) return QASA_OK;
+    if (!rotation->table || !block_table || !seq_lens || !k_new || !v_new || !k_new->data || !v_new->data)
+        return QASA_ERR_NULL;
+    if (q && (!q->data || !q_out)) return QASA_ERR_NULL;
+    if (batch < 0 || batch > 65535 || max_new_tokens < 0 || max_pages_per_seq < 1 ||
+        max_pages_per_seq > kMaxPagesPerSeq)
+        return QASA_ERR_SHAPE;
+    if (q && num_q_heads < 1) return QASA_ERR_SHAPE;
+    const long long per16 = 16 / (cache->dtype == QASA_DTYPE_F32 ? 4 : 2);   // elements of an input in 16 bytes
+    const qasa_token_rows *rows[3] = {k_new, v_new, q};
+    for (const qasa_token_rows *r : rows) {
+        if (!r) continue;
+        if (!aligned16(r->data)) return QASA_ERR_ALIGN;
+        if (batch > 1 && r->batch_stride < 0) return QASA_ERR_SHAPE;
+        if (max_new_tokens > 1 && r->token_stride < 0) return QASA_ERR_SHAPE;
+        if (batch > 1 && r->batch_stride % per16) return QASA_ERR_ALIGN;
+        if (max_new_tokens > 1 && r->token_stride % per16) return QASA_ERR_ALIGN;
+    }
+    if (!aligned16(rotation->table) || (q && !aligned16(q_out))) return QASA_ERR_ALIGN;
+    const void *words[] = {block_table, seq_lens, append_lens, device_status};
+    for (const void *w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
+    RotatedParams p;
+    p.k_pool = cache->k_pool;
+    p.v_pool = cache->v_pool;
+    p.bounds = cache->page_bounds;
+    p.scales = cache->page_scales;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.append_lens = append_lens;
+    p.table = rotation->table;
+    p.q = q ? q->data : nullptr;
+    p.q_out = q ? q_out : nullptr;
+    p.k_new = k_new->data;
+    p.v_new = v_new->data;
+    p.q_batch = q ? q->batch_stride : 0;
+    p.q_token = q ? q->token_stride : 0;
+    p.k_batch = k_new->batch_stride;
+    p.k_token = k_new->token_stride;
+    p.v_batch = v_new->batch_stride;
+    p.v_token = v_new->token_stride;
+    p.status = device_status;
+    p.num_phys = cache->num_phys_pages;
+    p.Hkv = cache->num_kv_heads;
+    p.Hq = q ? num_q_heads : 0;
+    p.P = cache->page_size;
+    p.max_pages = max_pages_per_seq;
+    p.T = max_new_tokens;
+    p.max_positions = rotation->max_positions;
+    p.rot = rotation->rot_dim;
+    p.interleaved = rotation->interleaved;
+    p.kv_blocks = 0;
+    const cudaError_t e = launch_append_rotated(cache->dtype, cache->head_dim, p, batch, stream);
+    if (e == cudaErrorInvalidConfiguration) return QASA_ERR_SHAPE;
+    return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+size_t qasa_window_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
+                                  int32_t max_q_tokens, int32_t max_pages_per_seq, int32_t window,
+                                  int32_t sink_tokens) {
+    (void)batch, (void)num_q_heads, (void)cache, (void)max_q_tokens, (void)max_pages_per_seq, (void)window;
+    (void)sink_tokens;
+    return 0;
+}
+
+qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
+                                  int32_t max_q_tokens, const int32_t *q_lens,
+                                  const int32_t *block_table, int32_t max_pages_per_seq,
+                                  const int32_t *seq_lens, int32_t window, int32_t sink_tokens,
+                                  float scale, void *out, void *workspace, size_t workspace_bytes,
+                                  int32_t batch, int32_t *device_status, cudaStream_t stream) {
+    if (window < 1 || sink_tokens < 0 || max_q_tokens < 0 || max_q_tokens > kMaxQueryTokens) {
+        const qasa_status st = check_cache(cache);
+        return st != QASA_OK ? st : QASA_ERR_SHAPE;
+    }
+    if (batch == 0 || max_q_tokens == 0) return check_cache(cache);
+    qasa_status st = check_decode(cache, q, num_q_heads, block_table, max_pages_per_seq, seq_lens, out, batch);
+    if (st != QASA_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(q_lens) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
+        return QASA_ERR_ALIGN;
+    const size_t need = qasa_window_workspace_size(batch, num_q_heads, cache, max_q_tokens, max_pages_per_seq, window,
+                                                   sink_tokens);
+    if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return QASA_ERR_WORKSPACE;
+    WindowParams p;
+    p.q = q;
+    p.out = out;
+    p.k_pool = cache->k_pool;
+    p.v_pool = cache->v_pool;
+    p.scales = cache->page_scales;
+    p.q_lens = q_lens;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.status = device_status;
+    p.B = batch;
+    p.T = max_q_tokens;
+    p.Hq = num_q_heads;
+    p.Hkv = cache->num_kv_heads;
+    p.G = num_q_heads / cache->num_kv_heads;
+    p.P = cache->page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_phys = cache->num_phys_pages;
+    p.window = window;
+    p.sinks = sink_tokens;
+    const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)cache->head_dim);
+    p.scale_log2 = (float)(sc * 1.4426950408889634);
+    p.row_tiles = 1;
+    const long long units = (long long)batch * p.Hkv * window_row_tiles(cache->dtype, p.T * p.G);
+    p.cluster = window_cluster(units, most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens));
+    if (units * p.cluster > 0x7fffffffLL) return QASA_ERR_SHAPE;
+    const cudaError_t e = launch_window_rows(cache->dtype, cache->head_dim, p, stream);
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 

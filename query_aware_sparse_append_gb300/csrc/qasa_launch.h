@@ -24,6 +24,42 @@ struct AppendParams {
     float *scales;       // FP8 KV: [num_phys][Hkv][4] (amax K, amax V, -, -)
 };
 
+struct RotatedParams {
+    void *k_pool;
+    void *v_pool;
+    void *bounds;
+    float *scales;       // FP8 KV: [num_phys][Hkv][4] (amax K, amax V, -, -)
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    const int32_t *append_lens;
+    const float *table;  // [max_positions][2][rot / 2]
+    const void *q;       // or NULL
+    void *q_out;
+    const void *k_new;
+    const void *v_new;
+    long long q_batch, q_token, k_batch, k_token, v_batch, v_token;   // strides in elements
+    int32_t *status;
+    int num_phys, Hkv, Hq, P, max_pages, T, max_positions, rot, interleaved;
+    int kv_blocks;       // blocks in x of the KV role, the rest rotate q
+};
+
+struct WindowParams {
+    const void *q;
+    void *out;
+    const void *k_pool;
+    const void *v_pool;
+    const float *scales; // FP8 KV: [num_phys][Hkv][4] (amax K, amax V, -, -)
+    const int32_t *q_lens;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int32_t *status;
+    int B, T, Hq, Hkv, G, P, max_pages, num_phys;
+    int window, sinks;
+    float scale_log2;
+    int cluster;         // CTAs that share a unit (row tile of a sequence and KV head)
+    int row_tiles;       // row tiles of the longest sequence
+};
+
 struct SelectParams {
     const void *bounds;
     const int32_t *block_table;
@@ -101,6 +137,11 @@ struct RebuildParams {
 };
 
 cudaError_t launch_append(qasa_dtype dt, int D, const AppendParams &p, int batch, cudaStream_t stream);
+cudaError_t launch_append_rotated(qasa_dtype dt, int D, const RotatedParams &p, int batch, cudaStream_t stream);
+// Windowed attention for few query rows per KV head; window_row_tiles: the units
+// per (sequence, KV head) that it makes of `rows` rows.
+int window_row_tiles(qasa_dtype dt, int rows);
+cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
 cudaError_t launch_select(qasa_dtype dt, int D, const SelectParams &p, int units, cudaStream_t stream);
 cudaError_t launch_attention(qasa_dtype dt, int D, int P, const CUtensorMap &km, const CUtensorMap &vm,
                              const AttnParams &p, int grid, size_t smem_budget, bool pdl,
