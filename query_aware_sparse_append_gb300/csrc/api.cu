@@ -386,6 +386,24 @@ qasa_status run_attention(const qasa_kv_cache *cache, const void *q, int num_q_h
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 
+// Rows (tokens x heads of a group) up to which the few-rows kernel serves a call.
+constexpr int kFewRows = 16;
+
+// View of 16-bit queries [tokens][heads][d] in boxes of 64 channels, one group's
+// heads and as many tokens as fill 128 rows.
+qasa_status query_tensor_map(CUtensorMap *map, const void *q, qasa_dtype dt, int d, int heads, int group, long long tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return QASA_ERR_DRIVER;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * heads};
+    cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, dt == QASA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           3, const_cast<void *>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QASA_OK : QASA_ERR_DRIVER;
+}
+
 // The most 16-token tiles that one query tile of a call can see.
 long long most_visible_tiles(int max_pages, int P, int T, int window, int sinks) {
     const long long all = (long long)max_pages * P / 16;
@@ -560,6 +578,23 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)cache->head_dim);
     p.scale_log2 = (float)(sc * 1.4426950408889634);
     p.row_tiles = 1;
+    p.cluster = 1;
+    p.wait_limit_ns = wait_limit_ns();
+    p.drain_limit_ns = kWaitLimitNs;
+    if (cache->dtype != QASA_DTYPE_F32 && p.T * p.G > kFewRows) {
+        CUtensorMap qm, km, vm;
+        st = query_tensor_map(&qm, q, cache->dtype, cache->head_dim, num_q_heads, p.G, (long long)batch * p.T);
+        if (st != QASA_OK) return st;
+        if (cache->dtype == QASA_DTYPE_E4M3) {
+            km = vm = qm;     // the codes do not come by TMA
+        } else {
+            st = pool_tensor_map(&km, cache->k_pool, cache, false);
+            if (st == QASA_OK) st = pool_tensor_map(&vm, cache->v_pool, cache, false);
+            if (st != QASA_OK) return st;
+        }
+        const cudaError_t pe = launch_window_prompt(cache->dtype, cache->head_dim, qm, km, vm, p, stream);
+        return pe == cudaSuccess ? QASA_OK : pe == cudaErrorInvalidConfiguration ? QASA_ERR_SHAPE : QASA_ERR_CUDA;
+    }
     const long long units = (long long)batch * p.Hkv * window_row_tiles(cache->dtype, p.T * p.G);
     p.cluster = window_cluster(units, most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens));
     if (units * p.cluster > 0x7fffffffLL) return QASA_ERR_SHAPE;

@@ -57,7 +57,9 @@ struct WindowParams {
     int window, sinks;
     float scale_log2;
     int cluster;         // CTAs that share a unit (row tile of a sequence and KV head)
-    int row_tiles;       // row tiles of the longest sequence
+    int row_tiles;       // row tiles (pairs of them in the prompt kernel) of the longest sequence
+    unsigned long long wait_limit_ns;    // prompt kernel: waits on other warps
+    unsigned long long drain_limit_ns;   // waits for the CTA's own copies and products (never shortened)
 };
 
 struct SelectParams {
@@ -142,6 +144,11 @@ cudaError_t launch_append_rotated(qasa_dtype dt, int D, const RotatedParams &p, 
 // per (sequence, KV head) that it makes of `rows` rows.
 int window_row_tiles(qasa_dtype dt, int rows);
 cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
+// The same for many: 16-bit and E4M3 caches.  q: [batch * tokens][heads][d] in boxes of
+// 64 channels, G heads and 128 / G tokens; k, v: pool rows in boxes of 64 channels and a
+// page's rows (not read for E4M3); 128-byte swizzle.
+cudaError_t launch_window_prompt(qasa_dtype dt, int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                                 const WindowParams &p, cudaStream_t stream);
 cudaError_t launch_select(qasa_dtype dt, int D, const SelectParams &p, int units, cudaStream_t stream);
 cudaError_t launch_attention(qasa_dtype dt, int D, int P, const CUtensorMap &km, const CUtensorMap &vm,
                              const AttnParams &p, int grid, size_t smem_budget, bool pdl,

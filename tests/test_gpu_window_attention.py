@@ -217,3 +217,22 @@ def test_repeats_bit_for_bit_and_replays_from_a_graph_on_another_stream(T):
         b = qasa.window_attention(cache, q, c.table, c.seq_lens, 300, 4, workspace=ws[0])
     torch.cuda.synchronize()
     assert torch.equal(a, out) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "e4m3"])
+def test_prompt_waits_with_a_short_limit_end_or_are_reported(dtype, monkeypatch):
+    # with a limit of 1 us a wait may give up (the hardware's own wait inside one attempt
+    # may also outlast it): the call ends by itself, right or reported, and the next one is right
+    qasa = _qasa()
+    c = R.Paged(dtype, [600, 300], 2, 128, 16, seed=20)
+    q = _queries(c, 300, 8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("QASA_WAIT_LIMIT_NS", "1000")
+    out = qasa.window_attention(c.library(), q, c.table, c.seq_lens, 200, 4, status=status)
+    torch.cuda.synchronize()
+    assert int(status) in (0, 0x8), hex(int(status))
+    if int(status) == 0:
+        _check(c, q, out, [300, 300], 200, 4)
+    monkeypatch.delenv("QASA_WAIT_LIMIT_NS")
+    out = _run(c, q, [300, 300], 200, 4, 300)
+    _check(c, q, out, [300, 300], 200, 4)
