@@ -585,13 +585,9 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
         CUtensorMap qm, km, vm;
         st = query_tensor_map(&qm, q, cache->dtype, cache->head_dim, num_q_heads, p.G, (long long)batch * p.T);
         if (st != QASA_OK) return st;
-        if (cache->dtype == QASA_DTYPE_E4M3) {
-            km = vm = qm;     // the codes do not come by TMA
-        } else {
-            st = pool_tensor_map(&km, cache->k_pool, cache, false);
-            if (st == QASA_OK) st = pool_tensor_map(&vm, cache->v_pool, cache, false);
-            if (st != QASA_OK) return st;
-        }
+        st = pool_tensor_map(&km, cache->k_pool, cache, false);
+        if (st == QASA_OK) st = pool_tensor_map(&vm, cache->v_pool, cache, false);
+        if (st != QASA_OK) return st;
         const cudaError_t pe = launch_window_prompt(cache->dtype, cache->head_dim, qm, km, vm, p, stream);
         return pe == cudaSuccess ? QASA_OK : pe == cudaErrorInvalidConfiguration ? QASA_ERR_SHAPE : QASA_ERR_CUDA;
     }

@@ -145,8 +145,8 @@ cudaError_t launch_append_rotated(qasa_dtype dt, int D, const RotatedParams &p, 
 int window_row_tiles(qasa_dtype dt, int rows);
 cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
 // The same for many: 16-bit and E4M3 caches.  q: [batch * tokens][heads][d] in boxes of
-// 64 channels, G heads and 128 / G tokens; k, v: pool rows in boxes of 64 channels and a
-// page's rows (not read for E4M3); 128-byte swizzle.
+// 64 channels, G heads and 128 / G tokens; k, v: pool rows in boxes of 64 channels (E4M3:
+// a whole row) and a page's rows; 128-byte swizzle (E4M3, d 64: none).
 cudaError_t launch_window_prompt(qasa_dtype dt, int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                  const WindowParams &p, cudaStream_t stream);
 cudaError_t launch_select(qasa_dtype dt, int D, const SelectParams &p, int units, cudaStream_t stream);

@@ -15,15 +15,19 @@
 //   warps 0-3, 4-7   one row tile each: a thread owns a row, reads its 128 scores
 //                    from tensor memory, and writes the weights back as the next
 //                    product's 16-bit operand over them; no shuffles
-//   warp 8           issues the products, S of one tile while the other tile's
-//                    softmax runs
-//   warp 9           brings pages by TMA into a ring of key and value tiles
-//   warps 12-15      E4M3 caches only: read codes, write f16 tiles into the ring
+//   warp 8           one thread issues the products, S of one tile while the other
+//                    tile's softmax runs
+//   warp 9           brings pages by TMA into a ring of key and value tiles (E4M3:
+//                    codes into a ring of their own)
+//   warp 10          hands value tiles on, hidden rows of edge tiles zeroed
+//   warps 12-15      E4M3 caches only: turn codes into f16 tiles of the ring
 // Tensor memory (512 columns): S0, S1 (P over them), O0, O1.
 //
-// The running maximum is raised only when a row's scores pass it by more than
-// 2^8: until then weights up to 256 are exact enough in 16 bits and fp32 sums, and
-// O needs no rescaling.
+// No maximum is sought where it is not needed: a tile's weights are taken against
+// the maximum so far, and only where a row's weights of the tile then sum to more
+// than 2^12 is the tile's own maximum found, O and the sum rescaled and the tile
+// done again.  Up to there nothing is lost: the sums are fp32, and 16-bit weights
+// keep their relative half step up to 2^12 as well as below 1.
 #include "tcgen05.cuh"
 #include "window.cuh"
 
@@ -33,22 +37,26 @@ namespace {
 
 constexpr int kRows = 128;            // rows of a row tile
 constexpr int kKeys = 128;            // tokens of a key tile
-constexpr float kSlack = 8.f;         // log2 units the scores may pass the running maximum
+constexpr float kMostWeight = 4096.f; // sum of a tile's weights from which on its maximum is sought
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
-template <int D> constexpr int ring_stages() { return D == 128 ? 5 : 8; }
-template <int D> constexpr size_t prompt_smem() {
-    return 1024 + (size_t)2 * kRows * D * 2 + (size_t)ring_stages<D>() * kv_bytes<D>();
+constexpr int kValueAhead = 4;        // value tiles handed on and not yet used: half the largest ring
+constexpr int kCodeStages = 2;        // key or value tiles of E4M3 codes under way
+template <int D, bool FP8> constexpr int ring_stages() { return FP8 ? 4 : D == 128 ? 5 : 8; }
+template <int D, bool FP8> constexpr size_t prompt_smem() {
+    return 1024 + (size_t)2 * kRows * D * 2 + (size_t)ring_stages<D, FP8>() * kv_bytes<D>() +
+           (FP8 ? (size_t)kCodeStages * kKeys * D : 0);
 }
 
 struct PromptShared {
-    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2], drained;
+    uint64_t q_full, kv_full[8], kv_empty[8], v_ready[kValueAhead], s_full[2], p_full[2], pv_done[2], drained;
+    uint64_t code_full[kCodeStages], code_empty[kCodeStages];
     uint32_t tmem;
     int any_bad;         // some page of this CTA has a bad block-table entry
     int failed;          // a bounded wait gave up: nothing is written
-    uint32_t vref;       // E4M3: bits of the largest V scale among the CTA's pages
-    float ks[kScaleRing][kKeys / 16], vs[kScaleRing][kKeys / 16];
+    uint32_t vmax;       // E4M3: bits of the largest V amax among the CTA's pages
+    float ks[kScaleRing][kKeys / 16], vamax[kScaleRing][kKeys / 16];
 };
 
 // Pages that some query at [first, last] sees: pages 0 .. head of the sinks, then pages body0 ..
@@ -92,23 +100,18 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         "mov.b64 {%0, %1}, a;\n\t}" : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
     return r;
 }
-__device__ __forceinline__ void mul2(uint32_t &x, uint32_t &y, float scale) {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\t"
-        "mov.b64 {%0, %1}, a;\n\t}" : "+r"(x), "+r"(y) : "f"(scale));
-}
-
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
 window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, WindowParams p) {
     constexpr int NB = D / 64;                        // 64-channel blocks
     constexpr int BLOCK = kRows * 128;                // bytes of one block of a tile
-    constexpr int NS = ring_stages<D>();
+    constexpr int NS = ring_stages<D, FP8>();
     constexpr uint32_t S_COL[2] = {0, 128}, O_COL[2] = {256, 256 + D};
 
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);   // the swizzle counts from 1 KB boundaries
-    unsigned char *qtile = smem, *ring = smem + 2 * NB * BLOCK;
+    unsigned char *qtile = smem, *ring = smem + 2 * NB * BLOCK, *codes = ring + NS * kv_bytes<D>();
     __shared__ PromptShared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -138,6 +141,11 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             mbar_init(&sh.kv_full[i], FP8 ? 128 : 1);
             mbar_init(&sh.kv_empty[i], 1);
         }
+        for (int i = 0; i < kValueAhead; ++i) mbar_init(&sh.v_ready[i], 1);
+        for (int i = 0; i < kCodeStages; ++i) {
+            mbar_init(&sh.code_full[i], 1);
+            mbar_init(&sh.code_empty[i], 128);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], kRows);
@@ -146,7 +154,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         mbar_init(&sh.drained, 1);
         sh.any_bad = 0;
         sh.failed = 0;
-        sh.vref = 0;
+        sh.vmax = 0;
         fence_barrier_init();
     }
     if (warp == 8) tmem_alloc(&sh.tmem, 512);
@@ -185,7 +193,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const int first = s.first + t0 + i * per, last = s.first + min(s.n, t0 + (i + 1) * per) - 1;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor memory lane of this warp, bits 16 up
         const uint32_t sa = tmem + lanes + S_COL[i], oa = tmem + lanes + O_COL[i];
-        float m = -INFINITY, l = 0.f;
+        float m = live ? -INFINITY : 0.f, l = 0.f;
         bool ok = true;
         // Whether every row of this row tile sees the whole key tile j.
         auto whole_tile = [&](int j) {
@@ -198,76 +206,92 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (!wait(&sh.s_full[i], j & 1)) { ok = false; break; }
             tc_fence_after();
             uint32_t x[kKeys];
-            tmem_ld32(sa, x);
-            tmem_ld32(sa + 32, x + 32);
-            tmem_ld32(sa + 64, x + 64);
-            tmem_ld32(sa + 96, x + 96);
-            tmem_wait_ld();
-            const bool bad = *(volatile int *)&sh.any_bad != 0;
-            if constexpr (FP8) {
+            bool raise = __any_sync(0xffffffffu, m == -INFINITY);       // a row has seen nothing yet
+            bool raised = false;
+            while (true) {
+                tmem_ld32(sa, x);
+                tmem_ld32(sa + 32, x + 32);
+                tmem_ld32(sa + 64, x + 64);
+                tmem_ld32(sa + 96, x + 96);
+                tmem_wait_ld();
+                const bool bad = *(volatile int *)&sh.any_bad != 0;
+                if (bad || !whole_tile(j)) {
+#pragma unroll
+                    for (int q = 0; q < kKeys / 16; ++q) {
+                        const int k = j * ppt + q * 16 / p.P, pg = pages.page(k);
+                        const int base = pg * p.P + q * 16 % p.P;
+                        uint32_t seen = 0;
+                        if (k < pages.count && (!bad || good_page(p, table, pg)))
+                            seen = upto16(pos, base) & (upto16(p.sinks - 1, base) | ~upto16(pos - p.window, base));
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (!(seen >> c & 1u)) x[q * 16 + c] = __float_as_uint(-INFINITY);
+                    }
+                }
+                if (raise) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < kKeys / 16; ++q) {
+                        float t[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            t[e] = fmaxf(fmaxf(__uint_as_float(x[q * 16 + e]), __uint_as_float(x[q * 16 + 4 + e])),
+                                         fmaxf(__uint_as_float(x[q * 16 + 8 + e]), __uint_as_float(x[q * 16 + 12 + e])));
+                        top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (FP8 ? sh.ks[j % kScaleRing][q] : 1.f));
+                    }
+                    const float m_new = fmaxf(m, top * p.scale_log2);
+                    const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
+                    m = m_new;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) { // the last product into O is complete: S of this tile follows it
+                            uint32_t o[32];
+                            tmem_ld32(oa + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(oa + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    raise = false;
+                    raised = true;
+                    continue;                             // the scores' registers were needed
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float2 sum[4] = {};
+                float vscale = 1.f;
+                if constexpr (FP8) {
+                    const float top = __uint_as_float(*(volatile uint32_t *)&sh.vmax);
+                    vscale = top > 0.f ? 1.f / top : 0.f;
+                }
 #pragma unroll
                 for (int q = 0; q < kKeys / 16; ++q) {
-                    const float ks = sh.ks[j % kScaleRing][q];
+                    float vs = 1.f, scale = p.scale_log2;
+                    if constexpr (FP8) {
+                        vs = sh.vamax[j % kScaleRing][q] * vscale;
+                        scale *= sh.ks[j % kScaleRing][q];
+                    }
 #pragma unroll
-                    for (int c = 0; c < 16; c += 2) mul2(x[q * 16 + c], x[q * 16 + c + 1], ks);
+                    for (int c = 0; c < 16; c += 2) {
+                        const int e = q * 16 + c;
+                        float2 w = fma2(x[e], x[e + 1], scale, -base);
+                        w.x = exp2_fast(w.x);
+                        w.y = exp2_fast(w.y);
+                        sum[c / 2 & 3] = add2(sum[c / 2 & 3], w);
+                        // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
+                        x[e / 2] = FP8 ? mma16816<T>::pack2(w.x * vs, w.y * vs) : mma16816<T>::pack2(w.x, w.y);
+                    }
                 }
-            }
-            if (bad || !whole_tile(j)) {
-#pragma unroll
-                for (int q = 0; q < kKeys / 16; ++q) {
-                    const int k = j * ppt + q * 16 / p.P, pg = pages.page(k);
-                    const int base = pg * p.P + q * 16 % p.P;
-                    uint32_t seen = 0;
-                    if (k < pages.count && (!bad || good_page(p, table, pg)))
-                        seen = upto16(pos, base) & (upto16(p.sinks - 1, base) | ~upto16(pos - p.window, base));
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (!(seen >> c & 1u)) x[q * 16 + c] = __float_as_uint(-INFINITY);
+                sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                const float add = sum[0].x + sum[0].y;
+                if (raised || !__any_sync(0xffffffffu, live && !(add <= kMostWeight))) {
+                    l += add;
+                    break;
                 }
+                raise = true;
             }
-            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    tops[e] = fmaxf(tops[e], fmaxf(__uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e])));
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.scale_log2;
-            if (j == 0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                const float m_new = fmaxf(m, top);
-                const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
-                m = m_new;
-                l *= f;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {     // the last product into O is complete: S of this tile follows it
-                    uint32_t o[32];
-                    tmem_ld32(oa + c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st32(oa + c, o);
-                }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            float2 sum[4] = {};
-#pragma unroll
-            for (int q = 0; q < kKeys / 16; ++q) {
-                float vs = 1.f;
-                if constexpr (FP8) vs = sh.vs[j % kScaleRing][q];
-#pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    const int e = q * 16 + c;
-                    float2 w = fma2(x[e], x[e + 1], p.scale_log2, -base);
-                    w.x = exp2_fast(w.x);
-                    w.y = exp2_fast(w.y);
-                    sum[c / 2 & 3] = add2(sum[c / 2 & 3], w);
-                    // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
-                    x[e / 2] = FP8 ? mma16816<T>::pack2(w.x * vs, w.y * vs) : mma16816<T>::pack2(w.x, w.y);
-                }
-            }
-            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += sum[0].x + sum[0].y;
             tmem_st32(sa, x);
             tmem_st32(sa + 32, x + 32);
             tmem_wait_st();
@@ -280,7 +304,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         if (ok) {
             float inv = l > 0.f ? 1.f / l : 0.f;      // a row that sees nothing is zero
-            if constexpr (FP8) inv *= __uint_as_float(*(volatile uint32_t *)&sh.vref);
+            if constexpr (FP8) inv *= fp8_scale(__uint_as_float(*(volatile uint32_t *)&sh.vmax));
             T *dst = static_cast<T *>(p.out) + (((size_t)b * p.T + tok) * p.Hq + h * p.G + g) * D;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
@@ -309,102 +333,78 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     } else if (warp == 8) {
         // ----------------------------------------------------------- products
         constexpr uint32_t qk = f16_idesc<T>(kRows, kKeys, false), pv = f16_idesc<T>(kRows, D, true);
-        const uint32_t q_addr = smem_u32(qtile), r_addr = smem_u32(ring);
-        auto scores = [&](int i, int stage) {
-            if (lane == 0) {
+        if (lane == 0) {
+            auto wait_one = [&](uint64_t *bar, uint32_t parity) {
+                if (mbar_wait_bounded(bar, parity, p.wait_limit_ns)) return true;
+                give_up();
+                return false;
+            };
+            const uint64_t qd = swz128_desc(smem_u32(qtile), 16, 1024), kd = swz128_desc(smem_u32(ring), 16, 1024);
+            const uint64_t vd = swz128_desc(smem_u32(ring), BLOCK, 1024);
+            auto scores = [&](int i, int stage) {
+                const uint64_t a = qd + (uint64_t)(i * NB * BLOCK >> 4), k0 = kd + (uint64_t)(stage * (kv_bytes<D>() >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * BLOCK + (k % 4) * 32;
-                    mma_ss(tmem + S_COL[i], swz128_desc(q_addr + i * NB * BLOCK + off, 16, 1024),
-                           swz128_desc(r_addr + stage * kv_bytes<D>() + off, 16, 1024), qk, k > 0);
+                    const uint64_t off = ((k / 4) * BLOCK + (k % 4) * 32) >> 4;
+                    mma_ss(tmem + S_COL[i], a + off, k0 + off, qk, k > 0);
                 }
                 tc_commit(&sh.s_full[i]);
-            }
-            __syncwarp();
-        };
-        auto output = [&](int i, int stage, bool add) {
-            if (lane == 0) {
+            };
+            auto output = [&](int i, int stage, bool add) {
+                const uint64_t v0 = vd + (uint64_t)(stage * (kv_bytes<D>() >> 4));
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tmem + O_COL[i], tmem + S_COL[i] + 8 * k,
-                           swz128_desc(r_addr + stage * kv_bytes<D>() + k * 2048, BLOCK, 1024), pv, add || k > 0);
+                    mma_ts(tmem + O_COL[i], tmem + S_COL[i] + 8 * k, v0 + (uint64_t)(k * 2048 >> 4), pv, add || k > 0);
                 tc_commit(&sh.pv_done[i]);
-            }
-            __syncwarp();
-        };
-        auto release = [&](int stage) {
-            if (lane == 0) tc_commit(&sh.kv_empty[stage]);
-            __syncwarp();
-        };
-        // Values that no row sees may be anything, and 0 * NaN is not 0: such rows
-        // of an edge tile become zeros.
-        auto clean = [&](int j, int stage) {
-            const bool bad = *(volatile int *)&sh.any_bad != 0;
-            bool any = bad || (j + 1) * ppt > pages.count;
-            for (int k = j * ppt; k < min((j + 1) * ppt, pages.count); ++k) {
-                const int base = pages.page(k) * p.P;
-                any |= base + p.P - 1 > pages.hi || (base < pages.lo && base + p.P > p.sinks);
-            }
-            if (!any) return;
-            for (int r = lane; r < kKeys; r += 32) {
-                const int k = j * ppt + r / p.P, pg = pages.page(k), at = pg * p.P + r % p.P;
-                const bool seen = k < pages.count && at <= pages.hi && (at >= pages.lo || at < p.sinks) &&
-                                  (!bad || good_page(p, table, pg));
-                if (!seen)
-#pragma unroll
-                    for (int c = 0; c < NB * 8; ++c)
-                        *reinterpret_cast<uint4 *>(ring + stage * kv_bytes<D>() + (c / 8) * BLOCK + r * 128 + c % 8 * 16) =
-                            make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            __syncwarp();
-        };
-        bool ok = n == 0 || (wait(&sh.q_full, 0) && wait(&sh.kv_full[0], 0));
-        if (ok && n > 0) {
-            tc_fence_after();
-            for (int i = 0; i < 2; ++i)
-                if (tiles[i] > 0) scores(i, 0);
-            release(0);
-        }
-        for (int j = 0; ok && j < n; ++j) {
-            const int vi = 2 * j + 1, ki = 2 * j + 2, vst = vi % NS, kst = ki % NS;
-            ok = wait(&sh.kv_full[vst], vi / NS & 1);
-            if (!ok) break;
-            if constexpr (!FP8) clean(j, vst);
-            bool have_k = false;
-            for (int i = 0; ok && i < 2; ++i) {
-                if (j >= tiles[i]) continue;
-                ok = wait(&sh.p_full[i], j & 1);
-                if (!ok) break;
+            };
+            bool ok = n == 0 || (wait_one(&sh.q_full, 0) && wait_one(&sh.kv_full[0], 0));
+            if (ok && n > 0) {
                 tc_fence_after();
-                output(i, vst, j > 0);
-                if (i == 1 || j >= tiles[1]) release(vst);
-                if (j + 1 < tiles[i]) {
-                    if (!have_k) {
-                        ok = wait(&sh.kv_full[kst], ki / NS & 1);
-                        have_k = true;
-                    }
-                    // the weights lie over the scores: they are free once the output product is complete
-                    ok = ok && wait(&sh.pv_done[i], j & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(i, kst);
-                }
+                for (int i = 0; i < 2; ++i)
+                    if (tiles[i] > 0) scores(i, 0);
+                tc_commit(&sh.kv_empty[0]);
             }
-            if (ok && have_k) release(kst);
+            for (int j = 0; ok && j < n; ++j) {
+                const int vi = 2 * j + 1, ki = 2 * j + 2, vst = vi % NS, kst = ki % NS;
+                const bool more = j + 1 < n;
+                ok = (FP8 ? wait_one(&sh.kv_full[vst], vi / NS & 1)
+                          : wait_one(&sh.v_ready[j % kValueAhead], j / kValueAhead & 1)) &&
+                     (!more || wait_one(&sh.kv_full[kst], ki / NS & 1));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!ok || j >= tiles[i]) continue;
+                    ok = wait_one(&sh.p_full[i], j & 1);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    output(i, vst, j > 0);
+                    if (i == 1 || j >= tiles[1]) tc_commit(&sh.kv_empty[vst]);
+                    if (j + 1 < tiles[i]) {
+                        // the weights lie over the scores: they are free once the output product is complete
+                        ok = wait_one(&sh.pv_done[i], j & 1);
+                        if (!ok) continue;
+                        tc_fence_after();
+                        scores(i, kst);
+                    }
+                }
+                if (ok && more) tc_commit(&sh.kv_empty[kst]);
+            }
+            // nothing of this CTA is under way when its tensor memory goes back
+            tc_commit(&sh.drained);
+            if (!mbar_wait_bounded(&sh.drained, 0, p.drain_limit_ns)) give_up();
         }
-        // nothing of this CTA is under way when its tensor memory goes back
-        if (lane == 0) tc_commit(&sh.drained);
         __syncwarp();
-        if (!mbar_wait_bounded(&sh.drained, 0, p.drain_limit_ns)) give_up();
-    } else if (!FP8 && warp == 9) {
+    } else if (warp == 9) {
         // -------------------------------------------------------- pages by TMA
+        // A lane brings one box of a tile: block lane % NB of page lane / NB, or
+        // the codes of page `lane`.
+        constexpr int BOXES = FP8 ? 1 : NB;
+        uint64_t *full = FP8 ? sh.code_full : sh.kv_full, *empty = FP8 ? sh.code_empty : sh.kv_empty;
+        constexpr int STAGES = FP8 ? kCodeStages : NS;
         if (lane == 0) {
             prefetch_tensormap(&qmap);
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);
         }
-        int issued = 0;
         if (n > 0) {
             if (lane == 0) {
                 const int q_tiles = tiles[1] > 0 ? 2 : 1;       // the first tile has rows; its keys may all be hidden
@@ -414,55 +414,87 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         tma_load_3d(qtile + (i * NB + c) * BLOCK, &qmap, &sh.q_full, c * 64, h * p.G,
                                     b * p.T + t0 + i * per);
             }
-            // a lane brings block lane % NB of page lane / NB of a tile
+            float2 amax = make_float2(0.f, 0.f);
             auto look_up = [&](int j) {
-                const int k = j * ppt + lane / NB;
-                if (lane >= ppt * NB || j >= n || k >= pages.count) return -1;
+                const int k = j * ppt + lane / BOXES;
+                if (lane >= ppt * BOXES || j >= n || k >= pages.count) return -1;
                 const int phys = table[pages.page(k)];
-                if (phys >= 0 && phys < p.num_phys) return phys;
+                if (phys >= 0 && phys < p.num_phys) {
+                    if constexpr (FP8) amax = *reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4);
+                    return phys;
+                }
                 *(volatile int *)&sh.any_bad = 1;
                 if (p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
                 return -1;
             };
-            int phys = look_up(0);
+            int phys = look_up(0), issued = 0;
             bool ok = true;
             for (int j = 0; ok && j < n; ++j) {
+                if constexpr (FP8) {
+                    // a page without keys has the scale 0, under which a hidden score's -inf would be NaN
+                    for (int q = lane * p.P / 16; lane < ppt && q < (lane + 1) * p.P / 16; ++q) {
+                        sh.ks[j % kScaleRing][q] = phys >= 0 ? fmaxf(fp8_scale(amax.x), 1e-30f) : 1.f;
+                        sh.vamax[j % kScaleRing][q] = phys >= 0 ? amax.y : 0.f;
+                    }
+                }
                 const int next = look_up(j + 1);
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, phys >= 0)) * p.P * 128;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, phys >= 0)) * p.P * (FP8 ? D : 128);
                 for (int v = 0; v < 2; ++v) {
-                    const int at = 2 * j + v, st = at % NS;
-                    ok = at < NS || wait(&sh.kv_empty[st], (at / NS - 1) & 1);
+                    const int at = 2 * j + v, st = at % STAGES;
+                    ok = at < STAGES || wait(&empty[st], (at / STAGES - 1) & 1);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], bytes);
                     __syncwarp();
-                    if (phys >= 0)
-                        tma_load_2d(ring + st * kv_bytes<D>() + (lane % NB) * BLOCK + (lane / NB) * p.P * 128,
-                                    v ? &vmap : &kmap, &sh.kv_full[st], (lane % NB) * 64, (phys * p.Hkv + h) * p.P);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                    __syncwarp();
+                    if (phys >= 0) {
+                        const int row = (phys * p.Hkv + h) * p.P;
+                        if constexpr (FP8)
+                            tma_load_2d(codes + st * kKeys * D + lane * p.P * D, v ? &vmap : &kmap, &full[st], 0, row);
+                        else
+                            tma_load_2d(ring + st * kv_bytes<D>() + (lane % NB) * BLOCK + (lane / NB) * p.P * 128,
+                                        v ? &vmap : &kmap, &full[st], (lane % NB) * 64, row);
+                    }
                     issued = at + 1;
                 }
                 phys = next;
             }
             // every copy has landed before the CTA may end
             if (!mbar_wait_bounded(&sh.q_full, 0, p.drain_limit_ns)) give_up();
-            for (int at = max(0, issued - NS); at < issued; ++at)
-                if (!mbar_wait_bounded(&sh.kv_full[at % NS], at / NS & 1, p.drain_limit_ns)) give_up();
+            for (int at = max(0, issued - STAGES); at < issued; ++at)
+                if (!mbar_wait_bounded(&full[at % STAGES], at / STAGES & 1, p.drain_limit_ns)) give_up();
         }
-    } else if (FP8 && warp == 9) {
-        if (n > 0) {
-            if (lane == 0) {
-                const int q_tiles = tiles[1] > 0 ? 2 : 1;
-                mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_tiles * NB * per * p.G * 128));
-                for (int i = 0; i < q_tiles; ++i)
-                    for (int c = 0; c < NB; ++c)
-                        tma_load_3d(qtile + (i * NB + c) * BLOCK, &qmap, &sh.q_full, c * 64, h * p.G,
-                                    b * p.T + t0 + i * per);
+    } else if (!FP8 && warp == 10) {
+        // ------------------------------------------------- value tiles handed on
+        // Values that no row sees may be anything, and 0 * NaN is not 0: such rows
+        // become zeros.  Only the last page, the pages where the sinks end and the
+        // window begins, and tiles with bad or no pages have them.
+        bool ok = true;
+        for (int j = 0; ok && j < n; ++j) {
+            const int vi = 2 * j + 1, st = vi % NS;
+            ok = wait(&sh.kv_full[st], vi / NS & 1);
+            if (!ok) break;
+            const bool bad = *(volatile int *)&sh.any_bad != 0;
+            const int k0 = j * ppt, k1 = k0 + ppt;
+            if (bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head)) {
+                for (int r = lane; r < kKeys; r += 32) {
+                    const int k = k0 + r / p.P, pg = pages.page(k), at = pg * p.P + r % p.P;
+                    const bool seen = k < pages.count && at <= pages.hi && (at >= pages.lo || at < p.sinks) &&
+                                      (!bad || good_page(p, table, pg));
+                    if (!seen)
+#pragma unroll
+                        for (int c = 0; c < NB * 8; ++c)
+                            *reinterpret_cast<uint4 *>(ring + st * kv_bytes<D>() + (c / 8) * BLOCK + r * 128 + c % 8 * 16) =
+                                make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
             }
-            if (!mbar_wait_bounded(&sh.q_full, 0, p.drain_limit_ns)) give_up();
+            if (lane == 0) mbar_arrive(&sh.v_ready[j % kValueAhead]);
         }
     } else if (FP8 && warp >= 12) {
         // --------------------------------------------- E4M3 codes to f16 tiles
         // Codes are exact in f16; the keys' scale multiplies the scores and the
-        // values' scale the weights, as a share of the largest one (vref), so that
+        // values' scale the weights, as a share of the largest one (vmax), so that
         // small scales lose nothing in 16 bits.
         constexpr int CPR = D / 16, RPI = 32 / CPR, IT = 32 / RPI;   // chunks per row, rows per step, steps
         const int cw = warp - 12, chunk = lane % CPR, rsub = lane / CPR;
@@ -473,73 +505,49 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) atomicMax(&sh.vref, __float_as_uint(fp8_scale(top)));
+        if (lane == 0) atomicMax(&sh.vmax, __float_as_uint(top));
         named_barrier_sync(1, 128);
-        const float vref = __uint_as_float(*(volatile uint32_t *)&sh.vref);
-        const unsigned char *pools[2] = {static_cast<const unsigned char *>(p.k_pool),
-                                         static_cast<const unsigned char *>(p.v_pool)};
-        // this warp's 32 rows of a tile: one page of 32 or two of 16
-        auto look_up = [&](int j, int &phys) {                       // lane x < 2: rows [16 x, 16 x + 16)
-            phys = -1;
-            const int k = j * ppt + (cw * 32 + (lane & 1) * 16) / p.P;
-            if (j < n && k < pages.count) {
-                const int t = table[pages.page(k)];
-                if (t >= 0 && t < p.num_phys) phys = t;
-                else {
-                    *(volatile int *)&sh.any_bad = 1;
-                    if (p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
-                }
-            }
-        };
-        uint4 w[IT];
-        auto fetch = [&](int v, int phys_x) {
+        bool ok = true;
+        for (int at = 0; ok && at < 2 * n; ++at) {
+            const int v = at & 1, j = at >> 1, cs = at % kCodeStages, st = at % NS;
+            ok = wait(&sh.code_full[cs], at / kCodeStages & 1);
+            if (!ok) break;
+            uint4 w[IT];
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-                const int r = it * RPI + rsub;                       // row of this warp's 32
-                const int phys = __shfl_sync(0xffffffffu, phys_x, r / 16);
-                w[it] = make_uint4(0, 0, 0, 0);
-                if (phys >= 0)
-                    w[it] = ld_global_nc_v4(pools[v] + (((size_t)phys * p.Hkv + h) * p.P + (cw * 32 + r) % p.P) * D + chunk * 16);
+                const int r = cw * 32 + it * RPI + rsub;
+                // 128-byte rows are swizzled
+                w[it] = *reinterpret_cast<const uint4 *>(codes + cs * kKeys * D + r * D +
+                                                         ((D == 128 ? chunk ^ (r & 7) : chunk) << 4));
             }
-        };
-        int phys = -1, next = -1;
-        look_up(0, phys);
-        if (n > 0) fetch(0, phys);
-        bool ok = true;
-        for (int j = 0; ok && j < n; ++j) {
-            look_up(j + 1, next);
-            if (lane < 2) {
-                float ks = 0.f, vs = 0.f;
-                if (phys >= 0) {
-                    const float2 a = *reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4);
-                    ks = fp8_scale(a.x);
-                    vs = vref > 0.f ? fp8_scale(a.y) / vref : 0.f;
-                }
-                sh.ks[j % kScaleRing][cw * 2 + lane] = ks;
-                sh.vs[j % kScaleRing][cw * 2 + lane] = vs;
-            }
-            for (int v = 0; v < 2; ++v) {
-                const int at = 2 * j + v, st = at % NS;
-                ok = at < NS || wait(&sh.kv_empty[st], (at / NS - 1) & 1);
-                if (!ok) break;
+            mbar_arrive(&sh.code_empty[cs]);
+            if (v) {
+                const bool bad = *(volatile int *)&sh.any_bad != 0;
+                const int k0 = j * ppt, k1 = k0 + ppt;
+                if (bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head)) {
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const int r = cw * 32 + it * RPI + rsub;
-                    if (v) {
-                        const int k = j * ppt + r / p.P, tok = pages.page(k) * p.P + r % p.P;
-                        if (tok > pages.hi || (tok < pages.lo && tok >= p.sinks)) w[it] = make_uint4(0, 0, 0, 0);
+                    for (int it = 0; it < IT; ++it) {                // as above: values that no row sees become zeros
+                        const int r = cw * 32 + it * RPI + rsub;
+                        const int k = k0 + r / p.P, pg = pages.page(k), tok = pg * p.P + r % p.P;
+                        const bool seen = k < pages.count && tok <= pages.hi && (tok >= pages.lo || tok < p.sinks) &&
+                                          (!bad || good_page(p, table, pg));
+                        if (!seen) w[it] = make_uint4(0, 0, 0, 0);
                     }
-                    uint4 a, c;
-                    e4m3x16_to_h(w[it], a, c);
-                    unsigned char *row = ring + st * kv_bytes<D>() + (chunk / 4) * BLOCK + r * 128;
-                    *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2) ^ (r & 7)) << 4)) = a;
-                    *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2 + 1) ^ (r & 7)) << 4)) = c;
                 }
-                fetch(1 - v, v ? next : phys);                       // the tile after this one
-                fence_async_smem();
-                mbar_arrive(&sh.kv_full[st]);
             }
-            phys = next;
+            ok = at < NS || wait(&sh.kv_empty[st], (at / NS - 1) & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int r = cw * 32 + it * RPI + rsub;
+                uint4 a, c;
+                e4m3x16_to_h(w[it], a, c);
+                unsigned char *row = ring + st * kv_bytes<D>() + (chunk / 4) * BLOCK + r * 128;
+                *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2) ^ (r & 7)) << 4)) = a;
+                *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2 + 1) ^ (r & 7)) << 4)) = c;
+            }
+            fence_async_smem();
+            mbar_arrive(&sh.kv_full[st]);
         }
     }
     tc_fence_before();
@@ -553,7 +561,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 template <typename T, bool FP8, int D>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, WindowParams p, cudaStream_t stream) {
     auto kernel = window_prompt_kernel<T, FP8, D>;
-    constexpr size_t smem = prompt_smem<D>();
+    constexpr size_t smem = prompt_smem<D, FP8>();
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int per = 2 * (kRows / p.G);
