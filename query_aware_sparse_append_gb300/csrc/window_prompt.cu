@@ -15,11 +15,15 @@
 //   warps 0-3, 4-7   one row tile each: a thread owns a row, reads its 128 scores
 //                    from tensor memory, and writes the weights back as the next
 //                    product's 16-bit operand over them; no shuffles
-//   warp 8           one thread issues the products, S of one tile while the other
-//                    tile's softmax runs
+//   warp 8           one thread issues the products, those of one tile while the
+//                    other tile's softmax runs; it is held while the tensor core is
+//                    busy, so each wait of its own is idle time there (two issuing
+//                    threads were slower: 435 against 336 us for the prompt below)
 //   warp 9           brings pages by TMA into a ring of key and value tiles (E4M3:
 //                    codes into a ring of their own)
-//   warp 10          hands value tiles on, hidden rows of edge tiles zeroed
+//   warp 10          zeroes hidden value rows of edge tiles, and waits for the tiles
+//                    in the issuing thread's place: the barrier of the weights takes
+//                    its arrival too
 //   warps 12-15      E4M3 caches only: turn codes into f16 tiles of the ring
 // Tensor memory (512 columns): S0, S1 (P over them), O0, O1.
 //
@@ -41,7 +45,6 @@ constexpr float kMostWeight = 4096.f; // sum of a tile's weights from which on i
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
-constexpr int kValueAhead = 4;        // value tiles handed on and not yet used: half the largest ring
 constexpr int kCodeStages = 2;        // key or value tiles of E4M3 codes under way
 template <int D, bool FP8> constexpr int ring_stages() { return FP8 ? 4 : D == 128 ? 5 : 8; }
 template <int D, bool FP8> constexpr size_t prompt_smem() {
@@ -50,7 +53,7 @@ template <int D, bool FP8> constexpr size_t prompt_smem() {
 }
 
 struct PromptShared {
-    uint64_t q_full, kv_full[8], kv_empty[8], v_ready[kValueAhead], s_full[2], p_full[2], pv_done[2], drained;
+    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2], drained;
     uint64_t code_full[kCodeStages], code_empty[kCodeStages];
     uint32_t tmem;
     int any_bad;         // some page of this CTA has a bad block-table entry
@@ -141,14 +144,13 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             mbar_init(&sh.kv_full[i], FP8 ? 128 : 1);
             mbar_init(&sh.kv_empty[i], 1);
         }
-        for (int i = 0; i < kValueAhead; ++i) mbar_init(&sh.v_ready[i], 1);
         for (int i = 0; i < kCodeStages; ++i) {
             mbar_init(&sh.code_full[i], 1);
             mbar_init(&sh.code_empty[i], 128);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], kRows);
+            mbar_init(&sh.p_full[i], kRows + 1);
             mbar_init(&sh.pv_done[i], 1);
         }
         mbar_init(&sh.drained, 1);
@@ -195,27 +197,31 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const uint32_t sa = tmem + lanes + S_COL[i], oa = tmem + lanes + O_COL[i];
         float m = live ? -INFINITY : 0.f, l = 0.f;
         bool ok = true;
-        // Whether every row of this row tile sees the whole key tile j.
-        auto whole_tile = [&](int j) {
-            const int k0 = j * ppt, k1 = k0 + ppt - 1;
-            if (k1 >= pages.count) return false;
-            const int base = pages.page(k0) * p.P, end = pages.page(k1) * p.P + p.P;     // the pages lie in between
-            return end - 1 <= first && (end <= p.sinks || base > last - p.window);
-        };
+        // Key tiles [whole0, whole1) are seen as a whole by every row of the row tile:
+        // full tiles of window pages up to the first row's position (tiles of sinks
+        // alone take the masked way).
+        int whole0 = 0, whole1 = 0;
+        if (first >= 0) {
+            const int clear = max(last - p.window + p.P, 0) / p.P;     // first page wholly inside the last row's window
+            whole0 = (pages.head + max(clear - pages.body0, 0) + ppt - 1) / ppt;
+            if (pages.head > 0) whole0 = max(whole0, (pages.head + ppt - 1) / ppt);
+            whole1 = (pages.head + max((first + 1) / p.P - pages.body0, 0)) / ppt;
+        }
+        bool unset = true;                    // a row of the warp has seen nothing yet
         for (int j = 0; j < tiles[i]; ++j) {
             if (!wait(&sh.s_full[i], j & 1)) { ok = false; break; }
             tc_fence_after();
             uint32_t x[kKeys];
-            bool raise = __any_sync(0xffffffffu, m == -INFINITY);       // a row has seen nothing yet
-            bool raised = false;
+            bool raise = unset, raised = false;
+            const bool bad = *(volatile int *)&sh.any_bad != 0;
+            const bool masked = bad || j < whole0 || j >= whole1;
             while (true) {
                 tmem_ld32(sa, x);
                 tmem_ld32(sa + 32, x + 32);
                 tmem_ld32(sa + 64, x + 64);
                 tmem_ld32(sa + 96, x + 96);
                 tmem_wait_ld();
-                const bool bad = *(volatile int *)&sh.any_bad != 0;
-                if (bad || !whole_tile(j)) {
+                if (masked) {
 #pragma unroll
                     for (int q = 0; q < kKeys / 16; ++q) {
                         const int k = j * ppt + q * 16 / p.P, pg = pages.page(k);
@@ -255,6 +261,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         }
                         tmem_wait_st();
                     }
+                    unset = __any_sync(0xffffffffu, m == -INFINITY);
                     raise = false;
                     raised = true;
                     continue;                             // the scores' registers were needed
@@ -360,20 +367,16 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             bool ok = n == 0 || (wait_one(&sh.q_full, 0) && wait_one(&sh.kv_full[0], 0));
             if (ok && n > 0) {
                 tc_fence_after();
-                for (int i = 0; i < 2; ++i)
-                    if (tiles[i] > 0) scores(i, 0);
+                if (tiles[0] > 0) scores(0, 0);
+                if (tiles[1] > 0) scores(1, 0);
                 tc_commit(&sh.kv_empty[0]);
             }
             for (int j = 0; ok && j < n; ++j) {
-                const int vi = 2 * j + 1, ki = 2 * j + 2, vst = vi % NS, kst = ki % NS;
-                const bool more = j + 1 < n;
-                ok = (FP8 ? wait_one(&sh.kv_full[vst], vi / NS & 1)
-                          : wait_one(&sh.v_ready[j % kValueAhead], j / kValueAhead & 1)) &&
-                     (!more || wait_one(&sh.kv_full[kst], ki / NS & 1));
+                const int vst = (2 * j + 1) % NS, kst = (2 * j + 2) % NS;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (!ok || j >= tiles[i]) continue;
-                    ok = wait_one(&sh.p_full[i], j & 1);
+                    ok = wait_one(&sh.p_full[i], j & 1);    // the weights, this value tile and the next key tile
                     if (!ok) continue;
                     tc_fence_after();
                     output(i, vst, j > 0);
@@ -386,7 +389,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         scores(i, kst);
                     }
                 }
-                if (ok && more) tc_commit(&sh.kv_empty[kst]);
+                if (ok && j + 1 < n) tc_commit(&sh.kv_empty[kst]);
             }
             // nothing of this CTA is under way when its tensor memory goes back
             tc_commit(&sh.drained);
@@ -463,11 +466,12 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             for (int at = max(0, issued - STAGES); at < issued; ++at)
                 if (!mbar_wait_bounded(&full[at % STAGES], at / STAGES & 1, p.drain_limit_ns)) give_up();
         }
-    } else if (!FP8 && warp == 10) {
-        // ------------------------------------------------- value tiles handed on
+    } else if (warp == 10) {
+        // --------------------------------------------------- tiles looked after
         // Values that no row sees may be anything, and 0 * NaN is not 0: such rows
-        // become zeros.  Only the last page, the pages where the sinks end and the
-        // window begins, and tiles with bad or no pages have them.
+        // become zeros (E4M3: when they are converted).  Only the last page, the
+        // pages where the sinks end and the window begins, and tiles with bad or no
+        // pages have them.
         bool ok = true;
         for (int j = 0; ok && j < n; ++j) {
             const int vi = 2 * j + 1, st = vi % NS;
@@ -475,7 +479,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (!ok) break;
             const bool bad = *(volatile int *)&sh.any_bad != 0;
             const int k0 = j * ppt, k1 = k0 + ppt;
-            if (bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head)) {
+            if (!FP8 && (bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head))) {
                 for (int r = lane; r < kKeys; r += 32) {
                     const int k = k0 + r / p.P, pg = pages.page(k), at = pg * p.P + r % p.P;
                     const bool seen = k < pages.count && at <= pages.hi && (at >= pages.lo || at < p.sinks) &&
@@ -489,7 +493,14 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 fence_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive(&sh.v_ready[j % kValueAhead]);
+            if (j + 1 < n) ok = wait(&sh.kv_full[(vi + 1) % NS], (vi + 1) / NS & 1);
+            // one arrival in each phase: not before the last one is over
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || j >= tiles[i]) continue;
+                ok = j == 0 || wait(&sh.p_full[i], (j - 1) & 1);
+                if (ok && lane == 0) mbar_arrive(&sh.p_full[i]);
+            }
         }
     } else if (FP8 && warp >= 12) {
         // --------------------------------------------- E4M3 codes to f16 tiles
@@ -520,7 +531,6 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 w[it] = *reinterpret_cast<const uint4 *>(codes + cs * kKeys * D + r * D +
                                                          ((D == 128 ? chunk ^ (r & 7) : chunk) << 4));
             }
-            mbar_arrive(&sh.code_empty[cs]);
             if (v) {
                 const bool bad = *(volatile int *)&sh.any_bad != 0;
                 const int k0 = j * ppt, k1 = k0 + ppt;
@@ -546,6 +556,9 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2) ^ (r & 7)) << 4)) = a;
                 *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2 + 1) ^ (r & 7)) << 4)) = c;
             }
+            // The codes go back only here: an arrival right after the loads overtakes
+            // them, and the next copy then lands before they have read.
+            mbar_arrive(&sh.code_empty[cs]);
             fence_async_smem();
             mbar_arrive(&sh.kv_full[st]);
         }
