@@ -412,13 +412,13 @@ long long most_visible_tiles(int max_pages, int P, int T, int window, int sinks)
     return seen < all ? seen : all;
 }
 
-// CTAs per unit of the few-rows kernel: as many as fill the SMs with four CTAs
-// each, while every warp has two tiles left.
+// CTAs per unit of the few-rows kernel: what fills the SMs with four CTAs each, so
+// that all run at once, as long as every warp has about four tiles.
 int window_cluster(long long units, long long tiles) {
     const int sms = sm_count() > 0 ? sm_count() : 152;
-    int c = 1;
-    while (c < 8 && units * c < 4LL * sms && tiles >= 4LL * 2 * 2 * c) c *= 2;
-    return c;
+    const long long fill = 4LL * sms / (units > 0 ? units : 1), work = tiles / 16;
+    const long long c = fill < work ? fill : work;
+    return c < 1 ? 1 : c > 8 ? 8 : (int)c;
 }
 
 }  // namespace

@@ -16,13 +16,16 @@
 // shared memory and the CTAs through distributed shared memory: no workspace, no
 // counters, one launch, and always in the same order.
 //
-// A warp's tile never passes through shared memory: K and V come by 16-byte loads
-// straight into the fragments of m16n8k16 products.  A lane's 16-byte chunk of a
+// Each warp has a ring of its own, filled by asynchronous 16-byte copies that hold
+// no registers: keys, values and the next keys are under way while it computes, and
+// four CTAs of four warps fit an SM, 128 KB and more in flight there (loads straight
+// into registers left two CTAs, 43 % of the copy rate).  Chunks go from the ring
+// into the fragments of m16n8k16 products as they are.  A lane's 16-byte chunk of a
 // key row is read as the pairs of k-steps; q's fragments take the same channel
 // order, and the sum over channels does not care about it.  Values need pairs of
-// tokens per channel: a lane loads the same channels of two neighbouring rows and
-// interleaves the halves with byte permutes.  The next tile's keys are under way
-// while the softmax runs, the next values while the next scores are computed.
+// tokens per channel: a lane takes the same channels of two neighbouring rows and
+// interleaves the halves with byte permutes.  As in the prompt kernel a step's
+// maximum is sought only where its weights grow large.
 #include "window.cuh"
 
 namespace qasa {
@@ -105,24 +108,48 @@ constexpr size_t rows_smem() { return (size_t)W * ROWS * D * 4 + (size_t)(W + 1)
 
 // ------------------------------------------------------- 16-bit and E4M3 pages
 
-// K and V of a tile, straight from the pool.
-template <bool FP8, int D> struct TileRegs {
-    static constexpr int KC = FP8 ? D / 64 : D / 32;   // 16-byte chunks of a key row per lane
-    static constexpr bool V8 = FP8 && D == 64;         // a lane's share of a value row is 8 bytes
-    static constexpr int VC = FP8 ? 1 : D / 64;        // chunks of a value row per lane
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+constexpr int kSlots = 3;                      // copies under way per warp: keys, values, the next keys
+constexpr float kMostWeight = 4096.f;          // sum of a step's weights from which on its maximum is sought
+
+// What a warp takes at once: `TPS` tiles, so that a copy is 4 KB (2 KB: E4M3, d 64).
+template <bool FP8, int D> struct Step {
+    static constexpr int ROWB = D * (FP8 ? 1 : 2);         // bytes of a row
+    static constexpr int TPS = ROWB == 256 ? 1 : 2;
+    static constexpr int BYTES = TPS * kTile * ROWB;
+    static constexpr int KC = ROWB / 64;                   // 16-byte chunks of a key row per lane
+    static constexpr bool V8 = ROWB == 64;                 // a lane's share of a value row is 8 bytes
+    static constexpr int VC = V8 ? 1 : ROWB / 128;         // chunks of a value row per lane
 };
+
+template <bool FP8, int D, int ROWS, int W>
+constexpr size_t step_smem() {
+    const size_t ring = (size_t)W * kSlots * Step<FP8, D>::BYTES;
+    return ring > rows_smem<D, ROWS, W>() ? ring : rows_smem<D, ROWS, W>();
+}
 
 // T: type of q and out; FP8: pages of E4M3 codes (T is __half).
 template <typename T, bool FP8, int D, int ROWS, int W>
-__global__ void __launch_bounds__(W * 32) window_rows_kernel(WindowParams p) {
-    using R = TileRegs<FP8, D>;
+__global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(WindowParams p) {
+    using R = Step<FP8, D>;
     constexpr bool TWO = ROWS == 16;          // rows 8 .. 15 of the products exist
+    constexpr int HALVES = TWO ? 2 : 1;
     constexpr int KS = D / 16;                // k-steps of the scores
     constexpr int NT = D / 8;                 // column tiles of the output
-    constexpr int ES = FP8 ? 1 : 2;
     constexpr int VCH = NT / R::VC;           // channels of a value chunk (8 or 16)
+    constexpr int TPS = R::TPS, ROWB = R::ROWB;
 
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     float *part_o = reinterpret_cast<float *>(smem);
     float2 *part_ml = reinterpret_cast<float2 *>(smem + (size_t)W * ROWS * D * 4);
 
@@ -136,13 +163,60 @@ __global__ void __launch_bounds__(W * 32) window_rows_kernel(WindowParams p) {
     if (rows <= 0) return;                    // the same for the whole cluster
     const int t0 = row0 / p.G, t1 = (row0 + rows - 1) / p.G;
     const VisibleTiles vis = visible_tiles(s.first + t0, s.first + t1, p.window, p.sinks);
+    const int32_t *table = p.block_table + (size_t)b * p.max_pages;
+
+    // This warp's tiles are number wg, wg + stride, ... of the visible ones.  Lane x
+    // holds the pool row (and scales) of tile from + x, and those of the 32 after.
+    const int stride = cluster * W, wg = rank * W + warp;
+    const int mine = vis.count > wg ? (vis.count - wg + stride - 1) / stride : 0;
+    const int steps = (mine + TPS - 1) / TPS;
+    struct Place { int row; float2 amax; };
+    auto look_up = [&](int x) {
+        Place a{-1, make_float2(0.f, 0.f)};
+        if (x < mine) {
+            int phys;
+            a.row = (int)tile_row(p, table, vis.tile(wg + x * stride), h, phys);      // below 2^31: checked on the host
+            if (FP8 && phys >= 0) a.amax = __ldg(reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4));
+        }
+        return a;
+    };
+    Place here = look_up(lane), there = look_up(32 + lane);
+    int from = 0;                              // `here` is tiles [from, from + 32)
 
     const int g4 = lane >> 2, q4 = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * kSlots * R::BYTES;
+    const unsigned char *pools[2] = {static_cast<const unsigned char *>(p.k_pool), static_cast<const unsigned char *>(p.v_pool)};
+    // Copy number c: keys (even) or values (odd) of step c / 2.  Chunks are spread so
+    // that the eight lanes of a shared-memory phase, which read two key rows or four
+    // value rows, meet different banks.
+    auto fetch = [&](int c, int slot) {
+        const int step = c >> 1, v = c & 1;
+        if (step < steps) {
+            const uint32_t dst = ring + slot * R::BYTES;
+#pragma unroll
+            for (int t = 0; t < TPS; ++t) {
+                const int x = step * TPS + t - from;              // at most one step past `here`
+                const int row = x < 32 ? __shfl_sync(0xffffffffu, here.row, x) : __shfl_sync(0xffffffffu, there.row, x - 32);
+                if (row < 0) continue;
+                const unsigned char *src = pools[v] + (size_t)row * ROWB + lane * 16;
+#pragma unroll
+                for (int it = 0; it < kTile * ROWB / 512; ++it) {
+                    const int id = it * 32 + lane, r = id / (ROWB / 16), ch = id % (ROWB / 16);
+                    const int f = ROWB == 64 ? 0 : v ? (r & 6) : (r & 1) << 2;
+                    copy16(dst + t * kTile * ROWB + r * ROWB + ((ch ^ f) << 4), src + it * 512);
+                }
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int c = 0; c < kSlots; ++c) fetch(c, c);
+
     // q fragments: rows g4 and g4 + 8, channels in the order of the key chunks
     uint32_t qa[KS][TWO ? 4 : 2];
-    int pos[TWO ? 2 : 1];                     // positions of this lane's rows
+    int pos[HALVES];                          // positions of this lane's rows
 #pragma unroll
-    for (int half = 0; half < (TWO ? 2 : 1); ++half) {
+    for (int half = 0; half < HALVES; ++half) {
         const int r = g4 + 8 * half;
         const bool live = r < rows;
         const int t = (row0 + (live ? r : 0)) / p.G, g = (row0 + (live ? r : 0)) % p.G;
@@ -155,225 +229,226 @@ __global__ void __launch_bounds__(W * 32) window_rows_kernel(WindowParams p) {
             uint4 w = make_uint4(0, 0, 0, 0);
             if (live) w = ld_global_nc_v4(row + c);
             qa[2 * j][half] = w.x;
-            qa[2 * j][half + (TWO ? 2 : 1)] = w.y;
+            qa[2 * j][half + HALVES] = w.y;
             qa[2 * j + 1][half] = w.z;
-            qa[2 * j + 1][half + (TWO ? 2 : 1)] = w.w;
+            qa[2 * j + 1][half + HALVES] = w.w;
         }
     }
 
-    float o[NT][TWO ? 4 : 2];
+    float o[NT][2 * HALVES];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < (TWO ? 4 : 2); ++e) o[n][e] = 0.f;
-    float m[TWO ? 2 : 1], l[TWO ? 2 : 1];
+        for (int e = 0; e < 2 * HALVES; ++e) o[n][e] = 0.f;
+    float m[HALVES], l[HALVES];
 #pragma unroll
-    for (int x = 0; x < (TWO ? 2 : 1); ++x) { m[x] = -INFINITY; l[x] = 0.f; }
+    for (int x = 0; x < HALVES; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
+    bool unset = true;                        // some row has seen nothing yet
     float vref = 0.f;                         // E4M3: o is in units of the largest V scale so far
 
-    const int32_t *table = p.block_table + (size_t)b * p.max_pages;
-    const int stride = cluster * W;
-    const int mine = vis.count > rank * W + warp ? (vis.count - (rank * W + warp) + stride - 1) / stride : 0;
+    int slot = 0;
+    for (int i = 0; i < steps; ++i) {
+        if (i * TPS - from >= 32) {
+            here = there;
+            from += 32;
+            there = look_up(from + 32 + lane);
+        }
+        int tok0[TPS];                        // first token of each tile
+        bool good[TPS];                       // the tile was brought
+        float ks[TPS], vs[TPS];
+#pragma unroll
+        for (int t = 0; t < TPS; ++t) {
+            const int x = i * TPS + t;
+            tok0[t] = vis.tile(wg + x * stride) * kTile;
+            good[t] = __shfl_sync(0xffffffffu, here.row, x - from) >= 0 && x < mine;
+            ks[t] = vs[t] = 1.f;
+            if constexpr (FP8) {
+                ks[t] = fp8_scale(__shfl_sync(0xffffffffu, here.amax.x, x - from));
+                vs[t] = fp8_scale(__shfl_sync(0xffffffffu, here.amax.y, x - from));
+            }
+        }
 
-    uint4 kr[2][R::KC];                       // key rows g4 and g4 + 8
-    uint4 vr[4][R::VC];                       // value rows 2 q4, 2 q4 + 1, + 8 (E4M3, d 64: low halves)
-    float ksc = 1.f, vsc = 1.f, ksc_next = 1.f, vsc_next = 1.f;
-
-    // lane x holds the place of this warp's tile (batch + x)
-    int batch = 0;
-    long long row_x = -1;
-    int phys_x = -1;
-    auto look_up = [&](int from) {
-        batch = from;
-        row_x = -1;
-        phys_x = -1;
-        if (from + lane < mine)
-            row_x = tile_row(p, table, vis.tile(rank * W + warp + (from + lane) * stride), h, phys_x);
-    };
-    const unsigned char *kpool = static_cast<const unsigned char *>(p.k_pool);
-    const unsigned char *vpool = static_cast<const unsigned char *>(p.v_pool);
-    auto load_k = [&](long long row) {
-        if (row < 0) return;
-        const unsigned char *base = kpool + (size_t)(row + g4) * D * ES + q4 * 16;
+        // scores
+        copy_wait<kSlots - 1>();
+        __syncwarp();
+        float sc[TPS][2][4];
+        uint32_t at = ring + slot * R::BYTES + g4 * ROWB;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int t = 0; t < TPS; ++t)
 #pragma unroll
-            for (int j = 0; j < R::KC; ++j) kr[x][j] = ld_global_nc_v4(base + x * 8 * D * ES + j * 64);
-    };
-    auto load_v = [&](long long row) {
-        if (row < 0) return;
-        const unsigned char *base = vpool + (size_t)(row + 2 * q4) * D * ES + g4 * (R::V8 ? 8 : 16);
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+                for (int e = 0; e < 4; ++e) sc[t][x][e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < R::VC; ++j) {
-                const unsigned char *a = base + ((x & 1) + 8 * (x >> 1)) * D * ES + j * 128;
-                if constexpr (R::V8) {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(a));
-                    vr[x][j] = make_uint4(w.x, w.y, 0, 0);
-                } else {
-                    vr[x][j] = ld_global_nc_v4(a);
+                for (int j = 0; j < R::KC; ++j) {
+                    const int f = ROWB == 64 ? 0 : (g4 & 1) << 2;
+                    const uint4 c = lds16(at + (t * kTile + x * 8) * ROWB + (((q4 + 4 * j) ^ f) << 4));
+                    uint32_t w[FP8 ? 8 : 4];
+                    if constexpr (FP8) {
+                        uint4 lo, hi;
+                        e4m3x16_to_h(c, lo, hi);
+                        w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+                        w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+                    } else {
+                        w[0] = c.x; w[1] = c.y; w[2] = c.z; w[3] = c.w;
+                    }
+#pragma unroll
+                    for (int k = 0; k < (FP8 ? 4 : 2); ++k) {
+                        const uint32_t *qk = qa[(FP8 ? 4 : 2) * j + k];
+                        const uint32_t a[4] = {qk[0], TWO ? qk[1] : 0u, qk[TWO ? 2 : 1], TWO ? qk[TWO ? 3 : 0] : 0u};
+                        mma16816<T>::run(sc[t][x], a, w[2 * k], w[2 * k + 1]);
+                    }
                 }
             }
-    };
-    auto scales_of = [&](int phys, float &k, float &v) {
-        if constexpr (FP8) {
-            if (phys < 0) return;
-            const float2 a = __ldg(reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4));
-            k = fp8_scale(a.x);
-            v = fp8_scale(a.y);
-        }
-    };
+        __syncwarp();
+        fetch(2 * i + kSlots, slot);
+        if (++slot == kSlots) slot = 0;
 
-    long long row = -1;
-    if (mine > 0) {
-        look_up(0);
-        row = __shfl_sync(0xffffffffu, row_x, 0);
-        scales_of(__shfl_sync(0xffffffffu, phys_x, 0), ksc, vsc);
-        load_k(row);
-        load_v(row);
-    }
-    for (int i = 0; i < mine; ++i) {
-        // where the next tile is
-        long long next = -1;
-        if (i + 1 < mine) {
-            if (i + 1 - batch == 32) look_up(i + 1);
-            next = __shfl_sync(0xffffffffu, row_x, i + 1 - batch);
-            scales_of(__shfl_sync(0xffffffffu, phys_x, i + 1 - batch), ksc_next, vsc_next);
-        }
-        const int tok0 = vis.tile(rank * W + warp + i * stride) * kTile;
-        float sc[2][4];
+        // weights
+        bool inside = true;                   // every row sees every token
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int t = 0; t < TPS; ++t)
+            inside = inside && good[t] && tok0[t] + kTile - 1 <= s.first + t0 &&
+                     (tok0[t] + kTile <= p.sinks || tok0[t] > s.first + t1 - p.window);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[x][e] = 0.f;
-        if (row >= 0) {
+        for (int t = 0; t < TPS; ++t)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    uint4 w;
-                    if constexpr (FP8) {
-                        const uint4 c = kr[x][j / 2];
-                        w = (j & 1) ? make_uint4(e4m3x2_to_h2(c.z), e4m3x2_to_h2(c.z >> 16), e4m3x2_to_h2(c.w),
-                                                 e4m3x2_to_h2(c.w >> 16))
-                                    : make_uint4(e4m3x2_to_h2(c.x), e4m3x2_to_h2(c.x >> 16), e4m3x2_to_h2(c.y),
-                                                 e4m3x2_to_h2(c.y >> 16));
-                    } else {
-                        w = kr[x][j];
-                    }
-                    uint32_t a[4];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        a[0] = qa[2 * j + k][0];
-                        a[1] = TWO ? qa[2 * j + k][1] : 0u;
-                        a[2] = qa[2 * j + k][TWO ? 2 : 1];
-                        a[3] = TWO ? qa[2 * j + k][TWO ? 3 : 1] : 0u;
-                        mma16816<T>::run(sc[x], a, k ? w.z : w.x, k ? w.w : w.y);
-                    }
+                for (int e = 0; e < 2 * HALVES; ++e) {
+                    sc[t][x][e] *= p.scale_log2 * ks[t];
+                    if (!inside && !(good[t] && sees(pos[e >> 1], tok0[t] + 8 * x + 2 * q4 + (e & 1), p.window, p.sinks)))
+                        sc[t][x][e] = -INFINITY;
                 }
+        if constexpr (FP8) {
+            float top = vs[0];
+#pragma unroll
+            for (int t = 1; t < TPS; ++t) top = fmaxf(top, vs[t]);
+            if (top > vref) {
+                const float g = vref / top;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2 * HALVES; ++e) o[n][e] *= g;
+                vref = top;
+            }
+#pragma unroll
+            for (int t = 0; t < TPS; ++t) vs[t] = vref > 0.f ? vs[t] / vref : 0.f;
         }
-        load_k(next);
+        uint32_t pa[TPS][4];
+        bool raise = unset;
+        while (true) {
+            if (raise) {                      // the step's own maximum
+#pragma unroll
+                for (int half = 0; half < HALVES; ++half) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < TPS; ++t)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) top = fmaxf(top, fmaxf(sc[t][x][2 * half], sc[t][x][2 * half + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float m_new = fmaxf(m[half], top);
+                    const float f = m_new == -INFINITY ? 1.f : exp2_fast(m[half] - m_new);
+                    m[half] = m_new;
+                    l[half] *= f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) { o[n][2 * half] *= f; o[n][2 * half + 1] *= f; }
+                }
+                bool none = m[0] == -INFINITY;
+                if constexpr (TWO) none = none || m[1] == -INFINITY;
+                unset = __any_sync(0xffffffffu, none);
+            }
+            float sum[HALVES];
+            bool small = true;
+#pragma unroll
+            for (int half = 0; half < HALVES; ++half) {
+                const float base = m[half] == -INFINITY ? 0.f : m[half];
+                sum[half] = 0.f;
+#pragma unroll
+                for (int t = 0; t < TPS; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float w0 = exp2_fast(sc[t][x][2 * half] - base), w1 = exp2_fast(sc[t][x][2 * half + 1] - base);
+                        sum[half] += w0 + w1;
+                        // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
+                        pa[t][half + 2 * x] = FP8 ? mma16816<T>::pack2(w0 * vs[t], w1 * vs[t]) : mma16816<T>::pack2(w0, w1);
+                    }
+                small = small && sum[half] <= kMostWeight;
+            }
+            if (raise || __all_sync(0xffffffffu, small)) {
+#pragma unroll
+                for (int half = 0; half < HALVES; ++half) l[half] += sum[half];
+                break;
+            }
+            raise = true;
+        }
 
-        if (row >= 0) {
-            const float to_log2 = p.scale_log2 * ksc;
-            // whole tile visible to every row of the unit?
-            const bool inside = tok0 + kTile - 1 <= s.first + t0 &&
-                                (tok0 + kTile <= p.sinks || tok0 > s.first + t1 - p.window);
-            uint32_t pa[4] = {0u, 0u, 0u, 0u};
-            float f[TWO ? 2 : 1];
-            float vscale = 1.f;
-            if constexpr (FP8) {
-                if (vsc > vref) {
-                    const float g = vref / vsc;
+        // output
+        copy_wait<kSlots - 1>();
+        __syncwarp();
+        at = ring + slot * R::BYTES + 2 * q4 * ROWB;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+        for (int t = 0; t < TPS; ++t) {
+            if constexpr (!TWO) pa[t][1] = pa[t][3] = 0u;
+            uint4 vr[4][R::VC];
 #pragma unroll
-                        for (int e = 0; e < (TWO ? 4 : 2); ++e) o[n][e] *= g;
-                    vref = vsc;
-                }
-                vscale = vref > 0.f ? vsc / vref : 0.f;
-            }
+            for (int x = 0; x < 4; ++x) {
+                const int r = 2 * q4 + (x & 1) + 8 * (x >> 1);
+                const uint32_t row = at + (t * kTile + (x & 1) + 8 * (x >> 1)) * ROWB;
 #pragma unroll
-            for (int half = 0; half < (TWO ? 2 : 1); ++half) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = sc[e >> 1][2 * half + (e & 1)] * to_log2;
-                    if (!inside && !sees(pos[half], tok0 + 8 * (e >> 1) + 2 * q4 + (e & 1), p.window, p.sinks))
-                        v[e] = -INFINITY;
-                }
-                float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float m_new = fmaxf(m[half], top);
-                const float base = m_new == -INFINITY ? 0.f : m_new;   // nothing seen yet: every weight is 0
-                f[half] = exp2_fast(m[half] - base);
-                m[half] = m_new;
-                float w[4], sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) { w[e] = exp2_fast(v[e] - base); sum += w[e]; }
-                l[half] = fmaf(l[half], f[half], sum);
-                // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
-                pa[half] = mma16816<T>::pack2(w[0] * vscale, w[1] * vscale);
-                pa[half + 2] = mma16816<T>::pack2(w[2] * vscale, w[3] * vscale);
-            }
-            bool same = f[0] == 1.f;
-            if constexpr (TWO) same = same && f[1] == 1.f;
-            if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[n][0] *= f[0];
-                    o[n][1] *= f[0];
-                    if constexpr (TWO) { o[n][2] *= f[1]; o[n][3] *= f[1]; }
-                }
-            }
-            if (!inside) {   // values that no row sees may be anything: 0 * NaN is not 0
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int j = tok0 + 2 * q4 + (x & 1) + 8 * (x >> 1);
-                    if (j > vis.hi || (j < vis.lo && j >= p.sinks))
-#pragma unroll
-                        for (int c = 0; c < R::VC; ++c) vr[x][c] = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < R::VC; ++c) {
+                    if constexpr (R::V8) {
+                        uint2 w;
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(row + g4 * 8));
+                        vr[x][c] = make_uint4(w.x, w.y, 0, 0);
+                    } else {
+                        vr[x][c] = lds16(row + (((g4 + 8 * c) ^ (r & 6)) << 4));
+                    }
+                    if (!inside) {            // values that no row sees may be anything: 0 * NaN is not 0
+                        const int j = tok0[t] + r;
+                        if (!good[t] || j > vis.hi || (j < vis.lo && j >= p.sinks)) vr[x][c] = make_uint4(0, 0, 0, 0);
+                    }
                 }
             }
 #pragma unroll
             for (int c = 0; c < R::VC; ++c)
 #pragma unroll
                 for (int k = 0; k < VCH / 2; ++k) {
-                    uint32_t r0, r1, r2, r3;
-                    if constexpr (FP8) {
-                        auto pick = [&](const uint4 &w) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 &w = vr[x][c];
+                        if constexpr (FP8) {
                             const uint32_t word = k / 2 == 0 ? w.x : k / 2 == 1 ? w.y : k / 2 == 2 ? w.z : w.w;
-                            return e4m3x2_to_h2(k & 1 ? word >> 16 : word);
-                        };
-                        r0 = pick(vr[0][c]); r1 = pick(vr[1][c]); r2 = pick(vr[2][c]); r3 = pick(vr[3][c]);
-                    } else {
-                        auto pick = [&](const uint4 &w) { return k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w; };
-                        r0 = pick(vr[0][c]); r1 = pick(vr[1][c]); r2 = pick(vr[2][c]); r3 = pick(vr[3][c]);
+                            r[x] = e4m3x2_to_h2(k & 1 ? word >> 16 : word);
+                        } else {
+                            r[x] = k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w;
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t sel = e ? 0x7632u : 0x5410u;
                         float *acc = o[c * VCH + 2 * k + e];
                         float d[4] = {acc[0], acc[1], TWO ? acc[TWO ? 2 : 0] : 0.f, TWO ? acc[TWO ? 3 : 0] : 0.f};
-                        mma16816<T>::run(d, pa, __byte_perm(r0, r1, sel), __byte_perm(r2, r3, sel));
+                        mma16816<T>::run(d, pa[t], __byte_perm(r[0], r[1], sel), __byte_perm(r[2], r[3], sel));
                         acc[0] = d[0];
                         acc[1] = d[1];
                         if constexpr (TWO) { acc[2] = d[2]; acc[3] = d[3]; }
                     }
                 }
         }
-        load_v(next);
-        row = next;
-        ksc = ksc_next;
-        vsc = vsc_next;
+        __syncwarp();
+        fetch(2 * i + 1 + kSlots, slot);
+        if (++slot == kSlots) slot = 0;
     }
 
-    // this warp's state: column tile c * VCH + idx, columns 2 q4 and 2 q4 + 1, is
-    // channel c * 8 VCH + VCH * column + idx
+    // this warp's state, over the rings: column tile c * VCH + idx, columns 2 q4 and
+    // 2 q4 + 1, is channel c * 8 VCH + VCH * column + idx
+    copy_wait<0>();
+    __syncthreads();
 #pragma unroll
-    for (int half = 0; half < (TWO ? 2 : 1); ++half) {
+    for (int half = 0; half < HALVES; ++half) {
         float sum = l[half];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -406,7 +481,7 @@ template <int D, int ROWS, int W>
 __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p) {
     constexpr int KC = D / 16;                 // float4 chunks of a key row per lane
     constexpr int VN = D / 32;                 // channels per lane
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     float *part_o = reinterpret_cast<float *>(smem);
     float2 *part_ml = reinterpret_cast<float2 *>(smem + (size_t)W * ROWS * D * 4);
     __shared__ __align__(16) float qs[ROWS][D];
@@ -556,11 +631,11 @@ cudaError_t launch_16(WindowParams p, cudaStream_t stream) {
     const int rows = p.T * p.G;
     if (rows <= 8) {
         p.row_tiles = 1;
-        return launch_rows(window_rows_kernel<T, FP8, D, 8, 4>, p, (long long)p.B * p.Hkv, 128, rows_smem<D, 8, 4>(), stream);
+        return launch_rows(window_rows_kernel<T, FP8, D, 8, 4>, p, (long long)p.B * p.Hkv, 128, step_smem<FP8, D, 8, 4>(), stream);
     }
     p.row_tiles = (rows + 15) / 16;
     return launch_rows(window_rows_kernel<T, FP8, D, 16, 4>, p, (long long)p.B * p.Hkv * p.row_tiles, 128,
-                       rows_smem<D, 16, 4>(), stream);
+                       step_smem<FP8, D, 16, 4>(), stream);
 }
 
 template <int D>
