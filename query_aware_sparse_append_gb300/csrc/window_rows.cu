@@ -20,12 +20,14 @@
 // no registers: keys, values and the next keys are under way while it computes, and
 // four CTAs of four warps fit an SM, 128 KB and more in flight there (loads straight
 // into registers left two CTAs, 43 % of the copy rate).  Chunks go from the ring
-// into the fragments of m16n8k16 products as they are.  A lane's 16-byte chunk of a
-// key row is read as the pairs of k-steps; q's fragments take the same channel
-// order, and the sum over channels does not care about it.  Values need pairs of
-// tokens per channel: a lane takes the same channels of two neighbouring rows and
-// interleaves the halves with byte permutes.  As in the prompt kernel a step's
-// maximum is sought only where its weights grow large.
+// into the fragments of m16n8k16 products as they are, tokens and channels as the 16
+// rows and the query rows as the 8 columns (the other way round half of every product
+// is empty at a group of 8).  A lane's 16-byte chunk of a key row is read as the pairs
+// of k-steps; q's fragments take the same channel order, and the sum over channels
+// does not care about it.  Values need pairs of tokens per channel: a lane takes the
+// same channels of two neighbouring rows and interleaves the halves with byte
+// permutes.  As in the prompt kernel a step's maximum is sought only where its
+// weights grow large.
 #include "window.cuh"
 
 namespace qasa {
@@ -122,6 +124,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 constexpr int kSlots = 3;                      // copies under way per warp: keys, values, the next keys
 constexpr float kMostWeight = 4096.f;          // sum of a step's weights from which on its maximum is sought
 
+// Four E4M3 codes as four halves, exactly.
+__device__ __forceinline__ void codes_to_h(uint32_t c, uint32_t *h) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]) : "r"(c));
+}
+
 // What a warp takes at once: `TPS` tiles, so that a copy is 4 KB (2 KB: E4M3, d 64).
 template <bool FP8, int D> struct Step {
     static constexpr int ROWB = D * (FP8 ? 1 : 2);         // bytes of a row
@@ -142,11 +150,9 @@ constexpr size_t step_smem() {
 template <typename T, bool FP8, int D, int ROWS, int W>
 __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(WindowParams p) {
     using R = Step<FP8, D>;
-    constexpr bool TWO = ROWS == 16;          // rows 8 .. 15 of the products exist
-    constexpr int HALVES = TWO ? 2 : 1;
+    constexpr int NH = ROWS / 8;              // query rows are the products' columns, 8 at a time
     constexpr int KS = D / 16;                // k-steps of the scores
-    constexpr int NT = D / 8;                 // column tiles of the output
-    constexpr int VCH = NT / R::VC;           // channels of a value chunk (8 or 16)
+    constexpr int VCH = D / 8 / R::VC;        // channels of a value chunk (8 or 16)
     constexpr int TPS = R::TPS, ROWB = R::ROWB;
 
     extern __shared__ __align__(128) unsigned char smem[];
@@ -170,13 +176,17 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
     const int stride = cluster * W, wg = rank * W + warp;
     const int mine = vis.count > wg ? (vis.count - wg + stride - 1) / stride : 0;
     const int steps = (mine + TPS - 1) / TPS;
-    struct Place { int row; float2 amax; };
+    struct Place { int row; float ks, vs; };
     auto look_up = [&](int x) {
-        Place a{-1, make_float2(0.f, 0.f)};
+        Place a{-1, 0.f, 0.f};
         if (x < mine) {
             int phys;
             a.row = (int)tile_row(p, table, vis.tile(wg + x * stride), h, phys);      // below 2^31: checked on the host
-            if (FP8 && phys >= 0) a.amax = __ldg(reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4));
+            if (FP8 && phys >= 0) {
+                const float2 amax = __ldg(reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4));
+                a.ks = fp8_scale(amax.x);
+                a.vs = fp8_scale(amax.y);
+            }
         }
         return a;
     };
@@ -212,15 +222,13 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
 #pragma unroll
     for (int c = 0; c < kSlots; ++c) fetch(c, c);
 
-    // q fragments: rows g4 and g4 + 8, channels in the order of the key chunks
-    uint32_t qa[KS][TWO ? 4 : 2];
-    int pos[HALVES];                          // positions of this lane's rows
+    // q fragments: query row 8 x + g4, channels in the order of the key chunks
+    uint32_t qb[NH][KS][2];
 #pragma unroll
-    for (int half = 0; half < HALVES; ++half) {
-        const int r = g4 + 8 * half;
+    for (int x = 0; x < NH; ++x) {
+        const int r = 8 * x + g4;
         const bool live = r < rows;
         const int t = (row0 + (live ? r : 0)) / p.G, g = (row0 + (live ? r : 0)) % p.G;
-        pos[half] = s.first + t;
         const T *row = static_cast<const T *>(p.q) + (((size_t)b * p.T + t) * p.Hq + h * p.G + g) * D;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
@@ -228,23 +236,42 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
             const int c = FP8 ? (q4 + 4 * (j / 2)) * 16 + 8 * (j & 1) : (q4 + 4 * j) * 8;
             uint4 w = make_uint4(0, 0, 0, 0);
             if (live) w = ld_global_nc_v4(row + c);
-            qa[2 * j][half] = w.x;
-            qa[2 * j][half + HALVES] = w.y;
-            qa[2 * j + 1][half] = w.z;
-            qa[2 * j + 1][half + HALVES] = w.w;
+            qb[x][2 * j][0] = w.x;
+            qb[x][2 * j][1] = w.y;
+            qb[x][2 * j + 1][0] = w.z;
+            qb[x][2 * j + 1][1] = w.w;
         }
     }
+    // a lane's scores and outputs belong to query rows 8 x + 2 q4 and the one after
+    int pos[NH][2];
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pos[x][e] = s.first + (row0 + min(8 * x + 2 * q4 + e, rows - 1)) / p.G;
 
-    float o[NT][2 * HALVES];
+    // o[c][u]: channels 2 u (elements 0, 1) and 2 u + 1 (2, 3) of this lane's chunk c
+    float o[R::VC][VCH / 2][NH][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int c = 0; c < R::VC; ++c)
 #pragma unroll
-        for (int e = 0; e < 2 * HALVES; ++e) o[n][e] = 0.f;
-    float m[HALVES], l[HALVES];
+        for (int u = 0; u < VCH / 2; ++u)
 #pragma unroll
-    for (int x = 0; x < HALVES; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
+            for (int x = 0; x < NH; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][u][x][e] = 0.f;
+    auto scale_o = [&](int x, float f0, float f1) {
+#pragma unroll
+        for (int c = 0; c < R::VC; ++c)
+#pragma unroll
+            for (int u = 0; u < VCH / 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][u][x][e] *= (e & 1) ? f1 : f0;
+    };
+    float m[NH][2], l[NH][2];
+#pragma unroll
+    for (int x = 0; x < NH; ++x) { m[x][0] = m[x][1] = -INFINITY; l[x][0] = l[x][1] = 0.f; }
     bool unset = true;                        // some row has seen nothing yet
-    float vref = 0.f;                         // E4M3: o is in units of the largest V scale so far
+    float vref = 0.f, inv_vref = 0.f;         // E4M3: o is in units of the largest V scale so far
 
     int slot = 0;
     for (int i = 0; i < steps; ++i) {
@@ -255,134 +282,152 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
         }
         int tok0[TPS];                        // first token of each tile
         bool good[TPS];                       // the tile was brought
-        float ks[TPS], vs[TPS];
+        bool inside = true;                   // every row sees every token
 #pragma unroll
         for (int t = 0; t < TPS; ++t) {
             const int x = i * TPS + t;
             tok0[t] = vis.tile(wg + x * stride) * kTile;
             good[t] = __shfl_sync(0xffffffffu, here.row, x - from) >= 0 && x < mine;
-            ks[t] = vs[t] = 1.f;
-            if constexpr (FP8) {
-                ks[t] = fp8_scale(__shfl_sync(0xffffffffu, here.amax.x, x - from));
-                vs[t] = fp8_scale(__shfl_sync(0xffffffffu, here.amax.y, x - from));
-            }
+            inside = inside && good[t] && tok0[t] + kTile - 1 <= s.first + t0 &&
+                     (tok0[t] + kTile <= p.sinks || tok0[t] > s.first + t1 - p.window);
         }
 
-        // scores
+        // scores: tokens g4 (elements 0, 1) and g4 + 8 (2, 3) of a tile
         copy_wait<kSlots - 1>();
         __syncwarp();
-        float sc[TPS][2][4];
+        float sc[TPS][NH][4];
         uint32_t at = ring + slot * R::BYTES + g4 * ROWB;
 #pragma unroll
-        for (int t = 0; t < TPS; ++t)
+        for (int t = 0; t < TPS; ++t) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < NH; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[t][x][e] = 0.f;
 #pragma unroll
-                for (int j = 0; j < R::KC; ++j) {
-                    const int f = ROWB == 64 ? 0 : (g4 & 1) << 2;
-                    const uint4 c = lds16(at + (t * kTile + x * 8) * ROWB + (((q4 + 4 * j) ^ f) << 4));
-                    uint32_t w[FP8 ? 8 : 4];
-                    if constexpr (FP8) {
-                        uint4 lo, hi;
-                        e4m3x16_to_h(c, lo, hi);
-                        w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-                        w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
-                    } else {
-                        w[0] = c.x; w[1] = c.y; w[2] = c.z; w[3] = c.w;
-                    }
+            for (int j = 0; j < R::KC; ++j) {
+                const int f = ROWB == 64 ? 0 : (g4 & 1) << 2;
+                const uint32_t chunk = at + t * kTile * ROWB + (((q4 + 4 * j) ^ f) << 4);
+                const uint4 c0 = lds16(chunk), c1 = lds16(chunk + 8 * ROWB);
+                constexpr int KW = FP8 ? 8 : 4;
+                uint32_t w0[KW], w1[KW];
+                if constexpr (FP8) {
+                    codes_to_h(c0.x, w0); codes_to_h(c0.y, w0 + 2); codes_to_h(c0.z, w0 + 4); codes_to_h(c0.w, w0 + 6);
+                    codes_to_h(c1.x, w1); codes_to_h(c1.y, w1 + 2); codes_to_h(c1.z, w1 + 4); codes_to_h(c1.w, w1 + 6);
+                } else {
+                    w0[0] = c0.x; w0[1] = c0.y; w0[2] = c0.z; w0[3] = c0.w;
+                    w1[0] = c1.x; w1[1] = c1.y; w1[2] = c1.z; w1[3] = c1.w;
+                }
 #pragma unroll
-                    for (int k = 0; k < (FP8 ? 4 : 2); ++k) {
-                        const uint32_t *qk = qa[(FP8 ? 4 : 2) * j + k];
-                        const uint32_t a[4] = {qk[0], TWO ? qk[1] : 0u, qk[TWO ? 2 : 1], TWO ? qk[TWO ? 3 : 0] : 0u};
-                        mma16816<T>::run(sc[t][x], a, w[2 * k], w[2 * k + 1]);
-                    }
+                for (int k = 0; k < KW / 2; ++k) {
+                    const uint32_t a[4] = {w0[2 * k], w1[2 * k], w0[2 * k + 1], w1[2 * k + 1]};
+#pragma unroll
+                    for (int x = 0; x < NH; ++x)
+                        mma16816<T>::run(sc[t][x], a, qb[x][KW / 2 * j + k][0], qb[x][KW / 2 * j + k][1]);
                 }
             }
+        }
         __syncwarp();
         fetch(2 * i + kSlots, slot);
         if (++slot == kSlots) slot = 0;
 
         // weights
-        bool inside = true;                   // every row sees every token
+        float vs[TPS];
 #pragma unroll
-        for (int t = 0; t < TPS; ++t)
-            inside = inside && good[t] && tok0[t] + kTile - 1 <= s.first + t0 &&
-                     (tok0[t] + kTile <= p.sinks || tok0[t] > s.first + t1 - p.window);
+        for (int t = 0; t < TPS; ++t) {
+            float to_log2 = p.scale_log2;
+            if constexpr (FP8) to_log2 *= __shfl_sync(0xffffffffu, here.ks, i * TPS + t - from);
 #pragma unroll
-        for (int t = 0; t < TPS; ++t)
+            for (int x = 0; x < NH; ++x)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+                for (int e = 0; e < 4; ++e) sc[t][x][e] *= to_log2;
+            vs[t] = 1.f;
+        }
+        if (!inside) {
 #pragma unroll
-                for (int e = 0; e < 2 * HALVES; ++e) {
-                    sc[t][x][e] *= p.scale_log2 * ks[t];
-                    if (!inside && !(good[t] && sees(pos[e >> 1], tok0[t] + 8 * x + 2 * q4 + (e & 1), p.window, p.sinks)))
-                        sc[t][x][e] = -INFINITY;
-                }
+            for (int t = 0; t < TPS; ++t)
+#pragma unroll
+                for (int x = 0; x < NH; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!good[t] || !sees(pos[x][e & 1], tok0[t] + 8 * (e >> 1) + g4, p.window, p.sinks))
+                            sc[t][x][e] = -INFINITY;
+        }
         if constexpr (FP8) {
-            float top = vs[0];
+            float top = 0.f;
 #pragma unroll
-            for (int t = 1; t < TPS; ++t) top = fmaxf(top, vs[t]);
+            for (int t = 0; t < TPS; ++t) {
+                vs[t] = __shfl_sync(0xffffffffu, here.vs, i * TPS + t - from);
+                top = fmaxf(top, vs[t]);
+            }
             if (top > vref) {
                 const float g = vref / top;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2 * HALVES; ++e) o[n][e] *= g;
+                for (int x = 0; x < NH; ++x) scale_o(x, g, g);
                 vref = top;
+                inv_vref = 1.f / top;
             }
 #pragma unroll
-            for (int t = 0; t < TPS; ++t) vs[t] = vref > 0.f ? vs[t] / vref : 0.f;
+            for (int t = 0; t < TPS; ++t) vs[t] *= inv_vref;
         }
-        uint32_t pa[TPS][4];
+        uint32_t pb[TPS][NH][2];
         bool raise = unset;
         while (true) {
             if (raise) {                      // the step's own maximum
+                bool none = false;
 #pragma unroll
-                for (int half = 0; half < HALVES; ++half) {
-                    float top = -INFINITY;
+                for (int x = 0; x < NH; ++x) {
+                    float f[2];
 #pragma unroll
-                    for (int t = 0; t < TPS; ++t)
+                    for (int e = 0; e < 2; ++e) {
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) top = fmaxf(top, fmaxf(sc[t][x][2 * half], sc[t][x][2 * half + 1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float m_new = fmaxf(m[half], top);
-                    const float f = m_new == -INFINITY ? 1.f : exp2_fast(m[half] - m_new);
-                    m[half] = m_new;
-                    l[half] *= f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) { o[n][2 * half] *= f; o[n][2 * half + 1] *= f; }
+                        for (int t = 0; t < TPS; ++t) top = fmaxf(top, fmaxf(sc[t][x][e], sc[t][x][2 + e]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float m_new = fmaxf(m[x][e], top);
+                        f[e] = m_new == -INFINITY ? 1.f : exp2_fast(m[x][e] - m_new);
+                        m[x][e] = m_new;
+                        l[x][e] *= f[e];
+                        none = none || m_new == -INFINITY;
+                    }
+                    scale_o(x, f[0], f[1]);
                 }
-                bool none = m[0] == -INFINITY;
-                if constexpr (TWO) none = none || m[1] == -INFINITY;
                 unset = __any_sync(0xffffffffu, none);
             }
-            float sum[HALVES];
+            float sum[NH][2];
             bool small = true;
 #pragma unroll
-            for (int half = 0; half < HALVES; ++half) {
-                const float base = m[half] == -INFINITY ? 0.f : m[half];
-                sum[half] = 0.f;
+            for (int x = 0; x < NH; ++x) {
+                const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
+                sum[x][0] = sum[x][1] = 0.f;
 #pragma unroll
                 for (int t = 0; t < TPS; ++t)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float w0 = exp2_fast(sc[t][x][2 * half] - base), w1 = exp2_fast(sc[t][x][2 * half + 1] - base);
-                        sum[half] += w0 + w1;
+                    for (int k = 0; k < 2; ++k) {
+                        float w0 = exp2_fast(sc[t][x][2 * k] - b0), w1 = exp2_fast(sc[t][x][2 * k + 1] - b1);
+                        sum[x][0] += w0;
+                        sum[x][1] += w1;
+                        if constexpr (FP8) { w0 *= vs[t]; w1 *= vs[t]; }
                         // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
-                        pa[t][half + 2 * x] = FP8 ? mma16816<T>::pack2(w0 * vs[t], w1 * vs[t]) : mma16816<T>::pack2(w0, w1);
+                        pb[t][x][k] = mma16816<T>::pack2(w0, w1);
                     }
-                small = small && sum[half] <= kMostWeight;
+                small = small && sum[x][0] <= kMostWeight && sum[x][1] <= kMostWeight;
             }
             if (raise || __all_sync(0xffffffffu, small)) {
 #pragma unroll
-                for (int half = 0; half < HALVES; ++half) l[half] += sum[half];
+                for (int x = 0; x < NH; ++x) { l[x][0] += sum[x][0]; l[x][1] += sum[x][1]; }
                 break;
             }
             raise = true;
         }
+        // from pairs of rows per token to pairs of tokens per row
+#pragma unroll
+        for (int t = 0; t < TPS; ++t)
+#pragma unroll
+            for (int x = 0; x < NH; ++x)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) pb[t][x][k] = movmatrix_trans(pb[t][x][k]);
 
         // output
         copy_wait<kSlots - 1>();
@@ -390,51 +435,45 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
         at = ring + slot * R::BYTES + 2 * q4 * ROWB;
 #pragma unroll
         for (int t = 0; t < TPS; ++t) {
-            if constexpr (!TWO) pa[t][1] = pa[t][3] = 0u;
             uint4 vr[4][R::VC];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int r = 2 * q4 + (x & 1) + 8 * (x >> 1);
-                const uint32_t row = at + (t * kTile + (x & 1) + 8 * (x >> 1)) * ROWB;
+            for (int y = 0; y < 4; ++y) {
+                const int r = 2 * q4 + (y & 1) + 8 * (y >> 1);
+                const uint32_t row = at + (t * kTile + (y & 1) + 8 * (y >> 1)) * ROWB;
 #pragma unroll
                 for (int c = 0; c < R::VC; ++c) {
                     if constexpr (R::V8) {
                         uint2 w;
                         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(row + g4 * 8));
-                        vr[x][c] = make_uint4(w.x, w.y, 0, 0);
+                        vr[y][c] = make_uint4(w.x, w.y, 0, 0);
                     } else {
-                        vr[x][c] = lds16(row + (((g4 + 8 * c) ^ (r & 6)) << 4));
+                        vr[y][c] = lds16(row + (((g4 + 8 * c) ^ (r & 6)) << 4));
                     }
                     if (!inside) {            // values that no row sees may be anything: 0 * NaN is not 0
                         const int j = tok0[t] + r;
-                        if (!good[t] || j > vis.hi || (j < vis.lo && j >= p.sinks)) vr[x][c] = make_uint4(0, 0, 0, 0);
+                        if (!good[t] || j > vis.hi || (j < vis.lo && j >= p.sinks)) vr[y][c] = make_uint4(0, 0, 0, 0);
                     }
                 }
             }
 #pragma unroll
             for (int c = 0; c < R::VC; ++c)
 #pragma unroll
-                for (int k = 0; k < VCH / 2; ++k) {
-                    uint32_t r[4];
+                for (int d = 0; d < VCH / (FP8 ? 4 : 2); ++d) {        // 32-bit words of a chunk
+                    uint32_t r[4][FP8 ? 2 : 1];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint4 &w = vr[x][c];
-                        if constexpr (FP8) {
-                            const uint32_t word = k / 2 == 0 ? w.x : k / 2 == 1 ? w.y : k / 2 == 2 ? w.z : w.w;
-                            r[x] = e4m3x2_to_h2(k & 1 ? word >> 16 : word);
-                        } else {
-                            r[x] = k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w;
-                        }
+                    for (int y = 0; y < 4; ++y) {
+                        const uint4 &w = vr[y][c];
+                        const uint32_t word = d == 0 ? w.x : d == 1 ? w.y : d == 2 ? w.z : w.w;
+                        if constexpr (FP8) codes_to_h(word, r[y]);
+                        else r[y][0] = word;
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t sel = e ? 0x7632u : 0x5410u;
-                        float *acc = o[c * VCH + 2 * k + e];
-                        float d[4] = {acc[0], acc[1], TWO ? acc[TWO ? 2 : 0] : 0.f, TWO ? acc[TWO ? 3 : 0] : 0.f};
-                        mma16816<T>::run(d, pa[t], __byte_perm(r[0], r[1], sel), __byte_perm(r[2], r[3], sel));
-                        acc[0] = d[0];
-                        acc[1] = d[1];
-                        if constexpr (TWO) { acc[2] = d[2]; acc[3] = d[3]; }
+                    for (int z = 0; z < (FP8 ? 2 : 1); ++z) {
+                        const uint32_t a[4] = {__byte_perm(r[0][z], r[1][z], 0x5410), __byte_perm(r[0][z], r[1][z], 0x7632),
+                                               __byte_perm(r[2][z], r[3][z], 0x5410), __byte_perm(r[2][z], r[3][z], 0x7632)};
+#pragma unroll
+                        for (int x = 0; x < NH; ++x)
+                            mma16816<T>::run(o[c][(FP8 ? 2 : 1) * d + z][x], a, pb[t][x][0], pb[t][x][1]);
                     }
                 }
         }
@@ -443,30 +482,30 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
         if (++slot == kSlots) slot = 0;
     }
 
-    // this warp's state, over the rings: column tile c * VCH + idx, columns 2 q4 and
-    // 2 q4 + 1, is channel c * 8 VCH + VCH * column + idx
+    // this warp's state, over the rings: chunk c of this lane is channels
+    // (8 c + g4) VCH ..
     copy_wait<0>();
     __syncthreads();
+    const float unitv = FP8 ? vref : 1.f;
 #pragma unroll
-    for (int half = 0; half < HALVES; ++half) {
-        float sum = l[half];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = g4 + 8 * half;
-        float *dst = part_o + ((size_t)warp * ROWS + r) * D;
-        const float unitv = FP8 ? vref : 1.f;
+    for (int x = 0; x < NH; ++x)
 #pragma unroll
-        for (int c = 0; c < R::VC; ++c)
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[x][e];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            const int r = 8 * x + 2 * q4 + e;
+            float *dst = part_o + ((size_t)warp * ROWS + r) * D;
 #pragma unroll
-            for (int col = 0; col < 2; ++col)
+            for (int c = 0; c < R::VC; ++c)
 #pragma unroll
-                for (int k = 0; k < VCH; k += 4)
-                    *reinterpret_cast<float4 *>(dst + c * 8 * VCH + VCH * (2 * q4 + col) + k) =
-                        make_float4(o[c * VCH + k][2 * half + col] * unitv, o[c * VCH + k + 1][2 * half + col] * unitv,
-                                    o[c * VCH + k + 2][2 * half + col] * unitv,
-                                    o[c * VCH + k + 3][2 * half + col] * unitv);
-        if (q4 == 0) part_ml[warp * ROWS + r] = make_float2(m[half], sum);
-    }
+                for (int u = 0; u < VCH / 2; u += 2)
+                    *reinterpret_cast<float4 *>(dst + (8 * c + g4) * VCH + 2 * u) =
+                        make_float4(o[c][u][x][e] * unitv, o[c][u][x][2 + e] * unitv, o[c][u + 1][x][e] * unitv,
+                                    o[c][u + 1][x][2 + e] * unitv);
+            if (g4 == 0) part_ml[warp * ROWS + r] = make_float2(m[x][e], sum);
+        }
     join_and_write<T, D, ROWS, W>(p, part_o, part_ml, cluster, row0, rows, b, h);
 }
 
