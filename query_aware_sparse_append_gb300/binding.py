@@ -197,9 +197,12 @@ class PagedKVCache:
         self.num_phys_pages, self.num_kv_heads, self.page_size, self.head_dim = n, hkv, p, d
         self.dtype = k_pool.dtype
         self.is_fp8 = fp8
+        self.value_dtype = torch.float16 if fp8 else self.dtype     # of queries, outputs and appended values
+        self.device_index = k_pool.get_device()                     # -1: not on a CUDA device
         self._c = _Cache(k_pool.data_ptr(), v_pool.data_ptr(), page_bounds.data_ptr(), n, hkv, p,
                          d, E4M3 if fp8 else DTYPE_IDS[k_pool.dtype],
                          page_scales.data_ptr() if fp8 else None)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, num_phys_pages: int, num_kv_heads: int, page_size: int, head_dim: int,
@@ -217,7 +220,7 @@ class PagedKVCache:
 
     @property
     def c_ref(self):
-        return ctypes.byref(self._c)
+        return self._ref
 
 
 def workspace_size(cache: PagedKVCache, batch: int, num_q_heads: int, max_pages_per_seq: int) -> int:
@@ -242,52 +245,46 @@ def kv_append(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Te
     _check(code, "qasa_kv_append")
 
 
-def _checked(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, device: torch.device):
-    """Address of a contiguous tensor of this type, shape and device (None: NULL)."""
+# The stream and device lookups below are the ones behind torch.cuda.current_stream()
+# and torch.cuda.current_device(), without the Stream object and the initialisation
+# check: a decode step's append takes less time than those do.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, index: int):
+    """Address of a contiguous tensor of this type and shape on CUDA device `index` (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d" % (name, dtype, tuple(shape), index))
 
 
-def _checked_status(status: Optional[torch.Tensor], device: torch.device):
+def _status_arg(status: Optional[torch.Tensor], index: int):
     if status is None:
         return None
-    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
-        raise ValueError("status must be an int32 tensor on %s" % device)
-    return status.data_ptr()
+    if status.dtype is torch.int32 and status.get_device() == index and status.numel() >= 1:
+        return status.data_ptr()
+    raise ValueError("status must be an int32 tensor on cuda:%d" % index)
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, head_dim: int, device: torch.device) -> _TokenRows:
-    if t.dim() != 4 or t.dtype != dtype or t.device != device or t.shape[3] != head_dim:
-        raise ValueError("%s must be a %s tensor [batch, tokens, heads, %d] on %s" % (name, dtype, head_dim, device))
+def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, head_dim: int, index: int) -> _TokenRows:
+    if t.dim() != 4 or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be a %s tensor [batch, tokens, heads, head_dim] on cuda:%d" % (name, dtype, index))
     sb, st, sh, sc = t.stride()
-    if (sc != 1 or (sh != head_dim and t.shape[2] > 1)) and t.numel():
+    if (sc != 1 or sh != head_dim) and t.numel() and (sc != 1 or t.shape[2] > 1):
         raise ValueError("the heads of a token of %s must be contiguous" % name)
     return _TokenRows(t.data_ptr(), sb, st)
 
 
-class _OnDevice:
-    """The stream of a call on `device`: the one given, else the device's current
-    one, with the device made current around the call where another one is."""
-
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        if device.type != "cuda":
-            raise ValueError("the cache must be on a CUDA device")
-        if stream is not None and stream.device != device:
-            raise ValueError("stream and cache are on different devices")
-        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """The stream of a call on device `index`: the one given, else the device's current one."""
+    if stream is None:
+        return _raw_stream(index)
+    if stream.device_index != index:
+        raise ValueError("stream and cache are on different devices")
+    return stream.cuda_stream
 
 
 def rotation_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -310,41 +307,44 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
     parts of one tensor: any batch and token stride that is a multiple of 16 bytes.  table: as made by
     rotation_table, whose last dimension says how many channels turn; interleaved: neighbouring
     channels are the pairs (else channels rot_dim / 2 apart)."""
-    dev = cache.k_pool.device
-    value = torch.float16 if cache.is_fp8 else cache.dtype
-    d = cache.head_dim
-    kr = _token_rows(k_new, "k_new", value, d, dev)
-    vr = _token_rows(v_new, "v_new", value, d, dev)
-    B, T, H = k_new.shape[:3]
-    if H != cache.num_kv_heads or v_new.shape != k_new.shape:
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return kv_append_rotated(cache, block_table, seq_lens, k_new, v_new, table, q, q_out, append_lens,
+                                     interleaved, status, stream)
+    value, d = cache.value_dtype, cache.head_dim
+    kr = _token_rows(k_new, "k_new", value, d, index)
+    vr = _token_rows(v_new, "v_new", value, d, index)
+    shape = k_new.shape
+    B, T, H, kd = shape
+    if H != cache.num_kv_heads or kd != d or v_new.shape != shape:
         raise ValueError("k_new and v_new must be [batch, tokens, num_kv_heads, head_dim]")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages_per_seq]")
     maxp = block_table.shape[1]
     if table.dim() != 3 or table.shape[1] != 2:
         raise ValueError("table must be [max_positions, 2, rot_dim / 2]")
-    rot = _Rotation(_checked(table, "table", torch.float32, table.shape, dev), table.shape[0], 2 * table.shape[2],
-                    1 if interleaved else 0)
-    qr = None
-    hq = 0
+    positions, _, half = angles = table.shape
+    rot = _Rotation(_arg(table, "table", torch.float32, angles, index), positions, 2 * half, 1 if interleaved else 0)
+    qr, hq, out = None, 0, None
     if q is not None:
-        qr = _token_rows(q, "q", value, d, dev)
-        hq = q.shape[2]
-        if q.shape[0] != B or q.shape[1] != T:
-            raise ValueError("q must have the batch and tokens of k_new")
+        qr = ctypes.byref(_token_rows(q, "q", value, d, index))
+        qb, qt, hq, qd = q.shape
+        if qb != B or qt != T or qd != d:
+            raise ValueError("q must have the batch and tokens of k_new and the cache's head_dim")
         if q_out is None:
-            q_out = torch.empty((B, T, hq, d), dtype=value, device=dev)
-        qr = ctypes.byref(qr)
+            q_out = torch.empty((B, T, hq, d), dtype=value, device=q.device)
+        out = _arg(q_out, "q_out", value, (B, T, hq, d), index)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _OnDevice(dev, stream) as on:
-        code = _lib.qasa_kv_append_rotated(
-            cache.c_ref, ctypes.byref(rot), _checked(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
-            _checked(seq_lens, "seq_lens", torch.int32, (B,), dev),
-            _checked(append_lens, "append_lens", torch.int32, (B,), dev), qr, hq,
-            _checked(q_out, "q_out", value, (B, T, hq, d), dev), ctypes.byref(kr), ctypes.byref(vr), B, T,
-            _checked_status(status, dev), on)
-    _check(code, "qasa_kv_append_rotated")
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    code = _lib.qasa_kv_append_rotated(
+        cache.c_ref, ctypes.byref(rot), _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), _arg(append_lens, "append_lens", torch.int32, (B,), index),
+        qr, hq, out, ctypes.byref(kr), ctypes.byref(vr), B, T, _status_arg(status, index), _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_kv_append_rotated")
     return q_out
 
 
@@ -368,9 +368,12 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
     holds the queries of the last q_lens[b] (default T) of its seq_lens[b] tokens, each of which sees
     itself and what came before within `window` tokens (None: everything) and the first `sink_tokens`.
     Rows at or past q_lens[b] of `out` are left as they were (unset where it is allocated here)."""
-    dev = cache.k_pool.device
-    value = torch.float16 if cache.is_fp8 else cache.dtype
-    shape = q.shape
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return window_attention(cache, q, block_table, seq_lens, window, sink_tokens, q_lens, scale, out, workspace,
+                                    status, stream)
+    value, shape = cache.value_dtype, q.shape
     if len(shape) == 4:
         B, T, hq, d = shape
     elif len(shape) == 3:
@@ -382,21 +385,23 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages_per_seq]")
     maxp = block_table.shape[1]
-    w = NO_WINDOW if window is None else int(window)
+    qp = _arg(q, "q", value, shape, index)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
         workspace = alloc_window_workspace(cache, B, hq, T, maxp, window, sink_tokens)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous memory on %s" % dev)
-    with _OnDevice(dev, stream) as on:
-        code = _lib.qasa_window_attention(
-            cache.c_ref, _checked(q, "q", value, shape, dev), hq, T, _checked(q_lens, "q_lens", torch.int32, (B,), dev),
-            _checked(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
-            _checked(seq_lens, "seq_lens", torch.int32, (B,), dev), w, int(sink_tokens), scale or 0.0,
-            _checked(out, "out", value, shape, dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            B, _checked_status(status, dev), on)
-    _check(code, "qasa_window_attention")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous memory on cuda:%d" % index)
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    code = _lib.qasa_window_attention(
+        cache.c_ref, qp, hq, T, _arg(q_lens, "q_lens", torch.int32, (B,), index),
+        _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), NO_WINDOW if window is None else window, sink_tokens,
+        scale or 0.0, _arg(out, "out", value, shape, index), workspace.data_ptr(), workspace.nbytes, B,
+        _status_arg(status, index), _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_window_attention")
     return out
 
 

@@ -142,8 +142,10 @@ template <bool FP8, int D> struct Step {
 
 template <bool FP8, int D, int ROWS, int W>
 constexpr size_t step_smem() {
-    const size_t ring = (size_t)W * kSlots * Step<FP8, D>::BYTES;
-    return ring > rows_smem<D, ROWS, W>() ? ring : rows_smem<D, ROWS, W>();
+    constexpr size_t ring = (size_t)W * kSlots * Step<FP8, D>::BYTES;
+    constexpr size_t most = ring > rows_smem<D, ROWS, W>() ? ring : rows_smem<D, ROWS, W>();
+    static_assert(most <= 48 << 10, "no opt-in needed");
+    return most;
 }
 
 // T: type of q and out; FP8: pages of E4M3 codes (T is __half).
@@ -520,6 +522,7 @@ template <int D, int ROWS, int W>
 __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p) {
     constexpr int KC = D / 16;                 // float4 chunks of a key row per lane
     constexpr int VN = D / 32;                 // channels per lane
+    constexpr int PARTS = ROWS == 1 ? 2 : 1;   // halves of a tile under way at once, as registers allow
     extern __shared__ __align__(128) unsigned char smem[];
     float *part_o = reinterpret_cast<float *>(smem);
     float2 *part_ml = reinterpret_cast<float2 *>(smem + (size_t)W * ROWS * D * 4);
@@ -536,6 +539,7 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
     if (rows <= 0) return;
     const int t0 = row0 / p.G, t1 = (row0 + rows - 1) / p.G;
     const VisibleTiles vis = visible_tiles(s.first + t0, s.first + t1, p.window, p.sinks);
+    const int32_t *table = p.block_table + (size_t)b * p.max_pages;
 
     for (int x = threadIdx.x; x < ROWS * D / 4; x += W * 32) {
         const int r = x / (D / 4), c = x % (D / 4);
@@ -558,36 +562,41 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
 #pragma unroll
         for (int e = 0; e < VN; ++e) o[r][e] = 0.f;
     }
-    const int32_t *table = p.block_table + (size_t)b * p.max_pages;
     const float *kpool = static_cast<const float *>(p.k_pool), *vpool = static_cast<const float *>(p.v_pool);
     const int stride = cluster * W;
-    for (int k = rank * W + warp; k < vis.count; k += stride) {
+    int k = rank * W + warp, phys;
+    long long base = k < vis.count ? tile_row(p, table, vis.tile(k), h, phys) : -1;
+    for (; k < vis.count; k += stride) {
         const int tile = vis.tile(k);
-        int phys;
-        const long long base = tile_row(p, table, tile, h, phys);
-        if (base < 0) continue;
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-            const int tok0 = tile * kTile + 8 * part;
-            const float *krow = kpool + (size_t)(base + 8 * part + g4) * D + q4 * 4;
-            float4 kc[KC];
+        const long long row = base;
+        if (k + stride < vis.count) base = tile_row(p, table, vis.tile(k + stride), h, phys);
+        if (row < 0) continue;
+        float4 kc[PARTS][KC];
+        float vv[PARTS][8][VN];
+        auto load = [&](int part, int slot) {          // 8 tokens
+            const float *krow = kpool + (size_t)(row + 8 * part + g4) * D + q4 * 4;
 #pragma unroll
-            for (int j = 0; j < KC; ++j) kc[j] = __ldg(reinterpret_cast<const float4 *>(krow + j * 16));
-            float vv[8][VN];
+            for (int j = 0; j < KC; ++j) kc[slot][j] = __ldg(reinterpret_cast<const float4 *>(krow + j * 16));
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                const float *vrow = vpool + (size_t)(base + 8 * part + t) * D + lane * VN;
-                const int j = tok0 + t;
+                const float *vrow = vpool + (size_t)(row + 8 * part + t) * D + lane * VN;
+                const int j = tile * kTile + 8 * part + t;
                 const bool any = j <= vis.hi && (j >= vis.lo || j < p.sinks);   // seen by some row
                 if constexpr (VN == 4) {
                     const float4 x = __ldg(reinterpret_cast<const float4 *>(vrow));
-                    vv[t][0] = any ? x.x : 0.f; vv[t][1] = any ? x.y : 0.f;
-                    vv[t][2] = any ? x.z : 0.f; vv[t][3] = any ? x.w : 0.f;
+                    vv[slot][t][0] = any ? x.x : 0.f; vv[slot][t][1] = any ? x.y : 0.f;
+                    vv[slot][t][2] = any ? x.z : 0.f; vv[slot][t][3] = any ? x.w : 0.f;
                 } else {
                     const float2 x = __ldg(reinterpret_cast<const float2 *>(vrow));
-                    vv[t][0] = any ? x.x : 0.f; vv[t][1] = any ? x.y : 0.f;
+                    vv[slot][t][0] = any ? x.x : 0.f; vv[slot][t][1] = any ? x.y : 0.f;
                 }
             }
+        };
+        if constexpr (PARTS == 2) { load(0, 0); load(1, 1); }
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const int tok0 = tile * kTile + 8 * part, slot = PARTS == 2 ? part : 0;
+            if constexpr (PARTS == 1) load(part, 0);
             float sc[ROWS];
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
@@ -595,8 +604,8 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
                     const float4 x = reinterpret_cast<const float4 *>(qs[r])[q4 + 4 * j];
-                    a = fmaf(kc[j].x, x.x, a); a = fmaf(kc[j].y, x.y, a);
-                    a = fmaf(kc[j].z, x.z, a); a = fmaf(kc[j].w, x.w, a);
+                    a = fmaf(kc[slot][j].x, x.x, a); a = fmaf(kc[slot][j].y, x.y, a);
+                    a = fmaf(kc[slot][j].z, x.z, a); a = fmaf(kc[slot][j].w, x.w, a);
                 }
                 a += __shfl_xor_sync(0xffffffffu, a, 1);
                 a += __shfl_xor_sync(0xffffffffu, a, 2);
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
                 for (int r = 0; r < ROWS; ++r) {
                     const float w = ps[warp][t][r];
 #pragma unroll
-                    for (int e = 0; e < VN; ++e) o[r][e] = fmaf(w, vv[t][e], o[r][e]);
+                    for (int e = 0; e < VN; ++e) o[r][e] = fmaf(w, vv[slot][t][e], o[r][e]);
                 }
             __syncwarp();
         }
@@ -649,8 +658,6 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
 
 template <typename K>
 cudaError_t launch_rows(K kernel, const WindowParams &p, long long units, int threads, size_t smem, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * p.cluster));
     cfg.blockDim = dim3(threads);
@@ -661,7 +668,7 @@ cudaError_t launch_rows(K kernel, const WindowParams &p, long long units, int th
     at[0].val.clusterDim.x = p.cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
