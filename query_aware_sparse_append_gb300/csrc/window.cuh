@@ -65,6 +65,12 @@ __device__ __forceinline__ long long tile_row(const WindowParams &p, const int32
     return ((long long)phys * p.Hkv + h) * p.P + (t % per_page) * kTile;
 }
 
+// Four E4M3 codes as four halves, exactly.
+__device__ __forceinline__ void codes_to_h(uint32_t c, uint32_t *h) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]) : "r"(c));
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {

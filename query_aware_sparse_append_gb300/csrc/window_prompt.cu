@@ -10,8 +10,8 @@
 // Rows: the G query heads of a KV head see the same keys, so a row tile packs
 // (token, head) rows, 128 / G tokens of G heads: the keys are shared by the whole
 // group and a tile spans few positions, which keeps partly hidden key tiles few.
-// A CTA owns two row tiles and goes through their visible pages, sinks first,
-// 128 tokens at a time:
+// A CTA owns two row tiles (NQ = 2; the warps below are numbered for it) and goes
+// through their visible pages, sinks first, 128 tokens at a time:
 //   warps 0-3, 4-7   one row tile each: a thread owns a row, reads its 128 scores
 //                    from tensor memory, and writes the weights back as the next
 //                    product's 16-bit operand over them; no shuffles
@@ -46,9 +46,9 @@ constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
 constexpr int kCodeStages = 2;        // key or value tiles of E4M3 codes under way
-template <int D, bool FP8> constexpr int ring_stages() { return FP8 ? 4 : D == 128 ? 5 : 8; }
-template <int D, bool FP8> constexpr size_t prompt_smem() {
-    return 1024 + (size_t)2 * kRows * D * 2 + (size_t)ring_stages<D, FP8>() * kv_bytes<D>() +
+template <int D, bool FP8, int NQ> constexpr int ring_stages() { return FP8 ? 4 : 5; }
+template <int D, bool FP8, int NQ> constexpr size_t prompt_smem() {
+    return 1024 + (size_t)NQ * kRows * D * 2 + (size_t)ring_stages<D, FP8, NQ>() * kv_bytes<D>() +
            (FP8 ? (size_t)kCodeStages * kKeys * D : 0);
 }
 
@@ -103,18 +103,25 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         "mov.b64 {%0, %1}, a;\n\t}" : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
     return r;
 }
-template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
+// NQ: row tiles of a CTA.  One where two CTAs fit an SM (16-bit pages of 64 channels):
+// each brings its own keys, but the first loads and the last stores of one run under
+// the other's products.
+template <bool FP8, int NQ> constexpr int prompt_threads() { return NQ * 128 + (FP8 ? 256 : 128); }
+
+template <typename T, bool FP8, int D, int NQ>
+__global__ void __launch_bounds__(prompt_threads<FP8, NQ>(), NQ == 1 ? 2 : 1)
 window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, WindowParams p) {
     constexpr int NB = D / 64;                        // 64-channel blocks
     constexpr int BLOCK = kRows * 128;                // bytes of one block of a tile
-    constexpr int NS = ring_stages<D, FP8>();
-    constexpr uint32_t S_COL[2] = {0, 128}, O_COL[2] = {256, 256 + D};
+    constexpr int NS = ring_stages<D, FP8, NQ>();
+    constexpr uint32_t S_COL[2] = {0, 128}, O_COL[2] = {NQ * 128, NQ * 128 + D}, TMEM = NQ * 256;
+    constexpr int MMA = 4 * NQ, LOAD = MMA + 1, KEEP = MMA + 2, CONVERT = MMA + 4;      // warps
+    static_assert(NQ == 2 || (!FP8 && D == 64), "registers and tensor memory of two CTAs");
 
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);   // the swizzle counts from 1 KB boundaries
-    unsigned char *qtile = smem, *ring = smem + 2 * NB * BLOCK, *codes = ring + NS * kv_bytes<D>();
+    unsigned char *qtile = smem, *ring = smem + NQ * NB * BLOCK, *codes = ring + NS * kv_bytes<D>();
     __shared__ PromptShared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -123,9 +130,9 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     const int pair = p.row_tiles - 1 - (int)(blockIdx.x / p.Hkv / p.B);
     const int per = kRows / p.G;                      // tokens of a row tile
     const QuerySpan s = query_span(p, b, h == 0 && pair == p.row_tiles - 1 && tid == 0);
-    const int t0 = pair * 2 * per;
+    const int t0 = pair * NQ * per;
     if (t0 >= s.n) return;
-    const int t_end = min(s.n, t0 + 2 * per);
+    const int t_end = min(s.n, t0 + NQ * per);
     const Pages pages = visible_pages(s.first + t0, s.first + t_end - 1, p.window, p.sinks, p.P);
     const int ppt = kKeys / p.P;                      // pages of a key tile
     const int32_t *table = p.block_table + (size_t)b * p.max_pages;
@@ -133,6 +140,8 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     int tiles[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        tiles[i] = 0;
+        if (i >= NQ) continue;
         const int last = s.first + min(s.n, t0 + (i + 1) * per) - 1;
         tiles[i] = t0 + i * per >= s.n || last < 0 ? 0 : (pages.head + max(last / p.P - pages.body0 + 1, 0) + ppt - 1) / ppt;
     }
@@ -159,7 +168,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         sh.vmax = 0;
         fence_barrier_init();
     }
-    if (warp == 8) tmem_alloc(&sh.tmem, 512);
+    if (warp == MMA) tmem_alloc(&sh.tmem, TMEM);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -175,17 +184,20 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         return false;
     };
     // registers go to the softmax warps, within what the block was launched with:
-    // 256 x 208 + 128 x 88 = 384 x 168, and 256 x 184 + 128 x 56 + 128 x 88 = 512 x 128
-    if (warp < 8) {
-        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // 256 x 208 + 128 x 88 = 384 x 168, 256 x 184 + 128 x 56 + 128 x 88 = 512 x 128,
+    // 128 x 184 + 128 x 72 = 256 x 128
+    if (warp < MMA) {
+        if constexpr (FP8 || NQ == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    } else if (FP8 && warp < 12) {
+    } else if (FP8 && warp < CONVERT) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    } else if (NQ == 1) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     }
 
-    if (warp < 8) {
+    if (warp < MMA) {
         // ------------------------------------------------------------ softmax
         const int i = warp >> 2;
         const int row = tid & 127;
@@ -337,7 +349,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 }
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == MMA) {
         // ----------------------------------------------------------- products
         constexpr uint32_t qk = f16_idesc<T>(kRows, kKeys, false), pv = f16_idesc<T>(kRows, D, true);
         if (lane == 0) {
@@ -396,7 +408,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (!mbar_wait_bounded(&sh.drained, 0, p.drain_limit_ns)) give_up();
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == LOAD) {
         // -------------------------------------------------------- pages by TMA
         // A lane brings one box of a tile: block lane % NB of page lane / NB, or
         // the codes of page `lane`.
@@ -466,7 +478,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             for (int at = max(0, issued - STAGES); at < issued; ++at)
                 if (!mbar_wait_bounded(&full[at % STAGES], at / STAGES & 1, p.drain_limit_ns)) give_up();
         }
-    } else if (warp == 10) {
+    } else if (warp == KEEP) {
         // --------------------------------------------------- tiles looked after
         // Values that no row sees may be anything, and 0 * NaN is not 0: such rows
         // become zeros (E4M3: when they are converted).  Only the last page, the
@@ -502,15 +514,15 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 if (ok && lane == 0) mbar_arrive(&sh.p_full[i]);
             }
         }
-    } else if (FP8 && warp >= 12) {
+    } else if (FP8 && warp >= CONVERT) {
         // --------------------------------------------- E4M3 codes to f16 tiles
         // Codes are exact in f16; the keys' scale multiplies the scores and the
         // values' scale the weights, as a share of the largest one (vmax), so that
         // small scales lose nothing in 16 bits.
         constexpr int CPR = D / 16, RPI = 32 / CPR, IT = 32 / RPI;   // chunks per row, rows per step, steps
-        const int cw = warp - 12, chunk = lane % CPR, rsub = lane / CPR;
+        const int cw = warp - CONVERT, chunk = lane % CPR, rsub = lane / CPR;
         float top = 0.f;
-        for (int k = tid - 384; k < pages.count; k += 128) {
+        for (int k = tid - 32 * CONVERT; k < pages.count; k += 128) {
             const int pg = pages.page(k);
             if (good_page(p, table, pg)) top = fmaxf(top, p.scales[((size_t)table[pg] * p.Hkv + h) * 4 + 1]);
         }
@@ -551,7 +563,10 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             for (int it = 0; it < IT; ++it) {
                 const int r = cw * 32 + it * RPI + rsub;
                 uint4 a, c;
-                e4m3x16_to_h(w[it], a, c);
+                codes_to_h(w[it].x, &a.x);
+                codes_to_h(w[it].y, &a.z);
+                codes_to_h(w[it].z, &c.x);
+                codes_to_h(w[it].w, &c.z);
                 unsigned char *row = ring + st * kv_bytes<D>() + (chunk / 4) * BLOCK + r * 128;
                 *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2) ^ (r & 7)) << 4)) = a;
                 *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2 + 1) ^ (r & 7)) << 4)) = c;
@@ -565,23 +580,24 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == MMA) {
         tc_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(tmem, TMEM);
     }
 }
 
 template <typename T, bool FP8, int D>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, WindowParams p, cudaStream_t stream) {
-    auto kernel = window_prompt_kernel<T, FP8, D>;
-    constexpr size_t smem = prompt_smem<D, FP8>();
+    constexpr int NQ = !FP8 && D == 64 ? 1 : 2;
+    auto kernel = window_prompt_kernel<T, FP8, D, NQ>;
+    constexpr size_t smem = prompt_smem<D, FP8, NQ>();
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int per = 2 * (kRows / p.G);
+    const int per = NQ * (kRows / p.G);
     p.row_tiles = (p.T + per - 1) / per;
     const long long blocks = (long long)p.row_tiles * p.B * p.Hkv;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kernel<<<(unsigned)blocks, FP8 ? 512 : 384, smem, stream>>>(q, k, v, p);
+    kernel<<<(unsigned)blocks, prompt_threads<FP8, NQ>(), smem, stream>>>(q, k, v, p);
     return cudaGetLastError();
 }
 

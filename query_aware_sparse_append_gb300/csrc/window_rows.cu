@@ -124,12 +124,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 constexpr int kSlots = 3;                      // copies under way per warp: keys, values, the next keys
 constexpr float kMostWeight = 4096.f;          // sum of a step's weights from which on its maximum is sought
 
-// Four E4M3 codes as four halves, exactly.
-__device__ __forceinline__ void codes_to_h(uint32_t c, uint32_t *h) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]) : "r"(c));
-}
-
 // What a warp takes at once: `TPS` tiles, so that a copy is 4 KB (2 KB: E4M3, d 64).
 template <bool FP8, int D> struct Step {
     static constexpr int ROWB = D * (FP8 ? 1 : 2);         // bytes of a row
