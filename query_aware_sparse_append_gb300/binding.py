@@ -390,6 +390,8 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
         out = torch.empty_like(q)
     if workspace is None:
         workspace = alloc_window_workspace(cache, B, hq, T, maxp, window, sink_tokens)
+        if stream is not None:
+            workspace.record_stream(stream)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous memory on cuda:%d" % index)
     if index < 0:

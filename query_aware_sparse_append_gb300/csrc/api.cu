@@ -386,8 +386,35 @@ qasa_status run_attention(const qasa_kv_cache *cache, const void *q, int num_q_h
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 
-// Rows (tokens x heads of a group) up to which the few-rows kernel serves a call.
-constexpr int kFewRows = 16;
+// Whether the few-rows kernel serves a call with this many rows (tokens x heads of a
+// group).  16-bit: what one of its row tiles holds; the prompt kernel takes a row tile
+// of 128 in the time it takes two of 16.  E4M3: up to the prompt kernel's row tile, as
+// that one has all visible pages unpacked first.  fp32: always, there is no other.
+bool window_few_rows(qasa_dtype dt, long long rows) {
+    return dt == QASA_DTYPE_F32 || rows <= (dt == QASA_DTYPE_E4M3 ? 128 : 16);
+}
+
+// Workspace of the prompt kernel for an E4M3 cache: the visible pages of `group`
+// sequences as halves, keys then values.  As many sequences as fit half a GiB go at
+// once, at least one.
+struct Unpacked {
+    int pages, group;
+    size_t bytes;
+};
+
+Unpacked window_unpacked(const qasa_kv_cache *c, int batch, int T, int max_pages, int window, int sinks) {
+    const long long P = c->page_size;
+    const long long seen = ((long long)window + T + P - 2) / P + 1 + ((long long)sinks + P - 1) / P;
+    Unpacked u;
+    u.pages = (int)(seen < max_pages ? seen : max_pages);
+    const long long one = 2LL * u.pages * c->num_kv_heads * P * c->head_dim * 2;
+    const long long rows = 0x7fffffffLL / ((long long)u.pages * c->num_kv_heads * P);   // tensor coordinates
+    long long g = (512LL << 20) / one;
+    if (g > rows) g = rows;
+    u.group = (int)(g < 1 ? 1 : g > batch ? batch : g);
+    u.bytes = (size_t)(one * u.group);
+    return u;
+}
 
 // View of 16-bit queries [tokens][heads][d] in boxes of 64 channels, one group's
 // heads and as many tokens as fill 128 rows.
@@ -533,9 +560,12 @@ qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotati
 size_t qasa_window_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
                                   int32_t max_q_tokens, int32_t max_pages_per_seq, int32_t window,
                                   int32_t sink_tokens) {
-    (void)batch, (void)num_q_heads, (void)cache, (void)max_q_tokens, (void)max_pages_per_seq, (void)window;
-    (void)sink_tokens;
-    return 0;
+    if (!cache || cache->dtype != QASA_DTYPE_E4M3 || batch < 1 || max_q_tokens < 1 || max_pages_per_seq < 1 ||
+        window < 1 || sink_tokens < 0 || cache->num_kv_heads < 1 || num_q_heads < cache->num_kv_heads ||
+        cache->page_size < 1 || cache->head_dim < 1)
+        return 0;
+    if (window_few_rows(cache->dtype, (long long)max_q_tokens * (num_q_heads / cache->num_kv_heads))) return 0;
+    return window_unpacked(cache, batch, max_q_tokens, max_pages_per_seq, window, sink_tokens).bytes;
 }
 
 qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
@@ -582,15 +612,34 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     p.cluster = 1;
     p.wait_limit_ns = wait_limit_ns();
     p.drain_limit_ns = kWaitLimitNs;
-    if (cache->dtype != QASA_DTYPE_F32 && p.T * p.G > kFewRows) {
+    p.b0 = 0;
+    p.ws_pages = 0;
+    if (!window_few_rows(cache->dtype, (long long)p.T * p.G)) {
         CUtensorMap qm, km, vm;
         st = query_tensor_map(&qm, q, cache->dtype, cache->head_dim, num_q_heads, p.G, (long long)batch * p.T);
         if (st != QASA_OK) return st;
-        st = pool_tensor_map(&km, cache->k_pool, cache, false);
-        if (st == QASA_OK) st = pool_tensor_map(&vm, cache->v_pool, cache, false);
+        qasa_kv_cache pages = *cache;             // what the tensor maps show
+        int group = batch;
+        if (cache->dtype == QASA_DTYPE_E4M3) {
+            const Unpacked u = window_unpacked(cache, batch, p.T, max_pages_per_seq, window, sink_tokens);
+            group = u.group;
+            p.ws_pages = u.pages;
+            pages.dtype = QASA_DTYPE_F16;
+            pages.num_phys_pages = u.group * u.pages;
+            pages.k_pool = workspace;
+            pages.v_pool = static_cast<unsigned char *>(workspace) + u.bytes / 2;
+        }
+        st = pool_tensor_map(&km, pages.k_pool, &pages, false);
+        if (st == QASA_OK) st = pool_tensor_map(&vm, pages.v_pool, &pages, false);
         if (st != QASA_OK) return st;
-        const cudaError_t pe = launch_window_prompt(cache->dtype, cache->head_dim, qm, km, vm, p, stream);
-        return pe == cudaSuccess ? QASA_OK : pe == cudaErrorInvalidConfiguration ? QASA_ERR_SHAPE : QASA_ERR_CUDA;
+        for (p.b0 = 0; p.b0 < batch; p.b0 += group) {
+            p.B = batch - p.b0 < group ? batch - p.b0 : group;
+            cudaError_t pe = cudaSuccess;
+            if (p.ws_pages) pe = launch_unpack_codes(cache->head_dim, p, pages.k_pool, pages.v_pool, stream);
+            if (pe == cudaSuccess) pe = launch_window_prompt(cache->dtype, cache->head_dim, qm, km, vm, p, stream);
+            if (pe != cudaSuccess) return pe == cudaErrorInvalidConfiguration ? QASA_ERR_SHAPE : QASA_ERR_CUDA;
+        }
+        return QASA_OK;
     }
     const long long units = (long long)batch * p.Hkv * window_row_tiles(cache->dtype, p.T * p.G);
     p.cluster = window_cluster(units, most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens));

@@ -59,6 +59,8 @@ struct WindowParams {
     float scale_log2;
     int cluster;         // CTAs that share a unit (row tile of a sequence and KV head)
     int row_tiles;       // row tiles (pairs of them in the prompt kernel) of the longest sequence
+    int b0;              // prompt kernel: first sequence of the launch, which has B of them
+    int ws_pages;        // E4M3, prompt kernel: pages per sequence in the workspace
     unsigned long long wait_limit_ns;    // prompt kernel: waits on other warps
     unsigned long long drain_limit_ns;   // waits for the CTA's own copies and products (never shortened)
 };
@@ -146,8 +148,10 @@ cudaError_t launch_append_rotated(qasa_dtype dt, int D, const RotatedParams &p, 
 int window_row_tiles(qasa_dtype dt, int rows);
 cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
 // The same for many: 16-bit and E4M3 caches.  q: [batch * tokens][heads][d] in boxes of
-// 64 channels, G heads and 128 / G tokens; k, v: pool rows in boxes of 64 channels (E4M3:
-// a whole row) and a page's rows; 128-byte swizzle (E4M3, d 64: none).
+// 64 channels, G heads and 128 / G tokens; k, v: pool rows (E4M3: the rows that
+// launch_unpack_codes has written) in boxes of 64 channels and a page's rows; 128-byte
+// swizzle.
+cudaError_t launch_unpack_codes(int D, const WindowParams &p, void *keys, void *values, cudaStream_t stream);
 cudaError_t launch_window_prompt(qasa_dtype dt, int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                  const WindowParams &p, cudaStream_t stream);
 cudaError_t launch_select(qasa_dtype dt, int D, const SelectParams &p, int units, cudaStream_t stream);

@@ -79,6 +79,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : QASA_R8(QASA_OUT, 0), QASA_R8(QASA_OUT, 8) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 QASA_R8(QASA_IN, 0), QASA_R8(QASA_IN, 8)
+                 : "memory");
+}
+
 #undef QASA_R8
 #undef QASA_OUT
 #undef QASA_IN

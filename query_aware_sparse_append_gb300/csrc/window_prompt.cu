@@ -5,33 +5,37 @@
 //
 // What bounds it: 4 d multiply-adds per visible (row, token) pair on the tensor
 // cores, and one exponential per pair on the other pipes; keys and values are
-// read once per 256 rows, from L2.
+// read once per 256 rows, from L2.  What it takes in fact is the chain of one row
+// tile, S -> softmax -> O -> next S, which the other tile's chain overlaps.
 //
 // Rows: the G query heads of a KV head see the same keys, so a row tile packs
 // (token, head) rows, 128 / G tokens of G heads: the keys are shared by the whole
 // group and a tile spans few positions, which keeps partly hidden key tiles few.
-// A CTA owns two row tiles (NQ = 2; the warps below are numbered for it) and goes
-// through their visible pages, sinks first, 128 tokens at a time:
-//   warps 0-3, 4-7   one row tile each: a thread owns a row, reads its 128 scores
-//                    from tensor memory, and writes the weights back as the next
-//                    product's 16-bit operand over them; no shuffles
-//   warp 8           one thread issues the products, those of one tile while the
-//                    other tile's softmax runs; it is held while the tensor core is
-//                    busy, so each wait of its own is idle time there (two issuing
-//                    threads were slower: 435 against 336 us for the prompt below)
-//   warp 9           brings pages by TMA into a ring of key and value tiles (E4M3:
-//                    codes into a ring of their own)
-//   warp 10          zeroes hidden value rows of edge tiles, and waits for the tiles
-//                    in the issuing thread's place: the barrier of the weights takes
-//                    its arrival too
-//   warps 12-15      E4M3 caches only: turn codes into f16 tiles of the ring
-// Tensor memory (512 columns): S0, S1 (P over them), O0, O1.
+// A CTA owns NQ row tiles and goes through their visible pages, sinks first, 128
+// tokens at a time.  Its warps, for NQ = 2:
+//   0-3, 4-7   one row tile each: a thread owns a row, reads its 128 scores from tensor
+//              memory, and writes the weights back as the next product's 16-bit operand
+//              over them; no shuffles (two threads to a row were slower, 342 against
+//              318 us for a prompt of 8192: the products then take twice as long)
+//   8          one thread issues the products, those of one tile while the other tile's
+//              softmax runs; it is held while the tensor core is busy, so each wait of
+//              its own is idle time there (two issuing threads: 435 against 336 us)
+//   9          brings pages by TMA into a ring of key and value tiles
+//   11         E4M3 caches: finds the largest value scale
+//   10         zeroes hidden value rows of edge tiles, and waits for the tiles in the
+//              issuing thread's place: the barrier of the weights takes its arrival too
+// Tensor memory: S0, S1 (P over them), O0, O1.
 //
 // No maximum is sought where it is not needed: a tile's weights are taken against
 // the maximum so far, and only where a row's weights of the tile then sum to more
 // than 2^12 is the tile's own maximum found, O and the sum rescaled and the tile
 // done again.  Up to there nothing is lost: the sums are fp32, and 16-bit weights
 // keep their relative half step up to 2^12 as well as below 1.
+//
+// E4M3 caches: a kernel before this one writes the codes of the pages in question as
+// halves, which they are exactly (converting them here, once per 256 rows, kept the
+// other warps waiting: 125 us for 2 x 2048 tokens over 1024).  The keys' scale then
+// multiplies the scores and the values' scale the weights.
 #include "tcgen05.cuh"
 #include "window.cuh"
 
@@ -45,20 +49,18 @@ constexpr float kMostWeight = 4096.f; // sum of a tile's weights from which on i
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
-constexpr int kCodeStages = 2;        // key or value tiles of E4M3 codes under way
-template <int D, bool FP8, int NQ> constexpr int ring_stages() { return FP8 ? 4 : 5; }
-template <int D, bool FP8, int NQ> constexpr size_t prompt_smem() {
-    return 1024 + (size_t)NQ * kRows * D * 2 + (size_t)ring_stages<D, FP8, NQ>() * kv_bytes<D>() +
-           (FP8 ? (size_t)kCodeStages * kKeys * D : 0);
+constexpr int kStages = 5;            // key and value tiles in the ring
+template <int D, int NQ> constexpr size_t prompt_smem() {
+    return 1024 + (size_t)NQ * kRows * D * 2 + (size_t)kStages * kv_bytes<D>();
 }
 
 struct PromptShared {
-    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2], drained;
-    uint64_t code_full[kCodeStages], code_empty[kCodeStages];
+    uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], pv_done[2], vmax_ready, drained;
     uint32_t tmem;
     int any_bad;         // some page of this CTA has a bad block-table entry
-    int failed;          // a bounded wait gave up: nothing is written
-    uint32_t vmax;       // E4M3: bits of the largest V amax among the CTA's pages
+    int failed;          // a bounded wait gave up: nothing more is written
+    int armed[kStages];  // copies into each stage so far
+    float vmax;          // E4M3: the largest V amax among the CTA's pages
     float ks[kScaleRing][kKeys / 16], vamax[kScaleRing][kKeys / 16];
 };
 
@@ -103,39 +105,41 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         "mov.b64 {%0, %1}, a;\n\t}" : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
     return r;
 }
-// NQ: row tiles of a CTA.  One where two CTAs fit an SM (16-bit pages of 64 channels):
-// each brings its own keys, but the first loads and the last stores of one run under
-// the other's products.
-template <bool FP8, int NQ> constexpr int prompt_threads() { return NQ * 128 + (FP8 ? 256 : 128); }
+// NQ: row tiles of a CTA.  One where two CTAs fit an SM (64 channels): each brings its
+// own keys, but the first loads and the last stores of one run under the other's
+// products.
+template <int NQ> constexpr int prompt_threads() { return NQ * 128 + 128; }
 
-template <typename T, bool FP8, int D, int NQ>
-__global__ void __launch_bounds__(prompt_threads<FP8, NQ>(), NQ == 1 ? 2 : 1)
+// T: 16-bit type of q, out and the pages; SCALED: pages of E4M3 values (as halves).
+template <typename T, bool SCALED, int D, int NQ>
+__global__ void __launch_bounds__(prompt_threads<NQ>(), NQ == 1 ? 2 : 1)
 window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, WindowParams p) {
     constexpr int NB = D / 64;                        // 64-channel blocks
     constexpr int BLOCK = kRows * 128;                // bytes of one block of a tile
-    constexpr int NS = ring_stages<D, FP8, NQ>();
+    constexpr int NS = kStages;
     constexpr uint32_t S_COL[2] = {0, 128}, O_COL[2] = {NQ * 128, NQ * 128 + D}, TMEM = NQ * 256;
-    constexpr int MMA = 4 * NQ, LOAD = MMA + 1, KEEP = MMA + 2, CONVERT = MMA + 4;      // warps
-    static_assert(NQ == 2 || (!FP8 && D == 64), "registers and tensor memory of two CTAs");
+    constexpr int MMA = 4 * NQ, LOAD = MMA + 1, KEEP = MMA + 2, LARGEST = MMA + 3;      // warps
+    static_assert(NQ == 2 || D == 64, "tensor memory of two CTAs");
 
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);   // the swizzle counts from 1 KB boundaries
-    unsigned char *qtile = smem, *ring = smem + NQ * NB * BLOCK, *codes = ring + NS * kv_bytes<D>();
+    unsigned char *qtile = smem, *ring = smem + NQ * NB * BLOCK;
     __shared__ PromptShared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // later positions first: they see the most keys
     const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv % p.B;
     const int pair = p.row_tiles - 1 - (int)(blockIdx.x / p.Hkv / p.B);
+    const int seq = p.b0 + b;                         // E4M3: the workspace holds some sequences at a time
     const int per = kRows / p.G;                      // tokens of a row tile
-    const QuerySpan s = query_span(p, b, h == 0 && pair == p.row_tiles - 1 && tid == 0);
+    const QuerySpan s = query_span(p, seq, h == 0 && pair == p.row_tiles - 1 && tid == 0);
     const int t0 = pair * NQ * per;
     if (t0 >= s.n) return;
     const int t_end = min(s.n, t0 + NQ * per);
     const Pages pages = visible_pages(s.first + t0, s.first + t_end - 1, p.window, p.sinks, p.P);
     const int ppt = kKeys / p.P;                      // pages of a key tile
-    const int32_t *table = p.block_table + (size_t)b * p.max_pages;
+    const int32_t *table = p.block_table + (size_t)seq * p.max_pages;
     // key tiles that each row tile goes through: up to its last position
     int tiles[2];
 #pragma unroll
@@ -150,13 +154,11 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     if (tid == 0) {
         mbar_init(&sh.q_full, 1);
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&sh.kv_full[i], FP8 ? 128 : 1);
+            mbar_init(&sh.kv_full[i], 1);
             mbar_init(&sh.kv_empty[i], 1);
+            sh.armed[i] = 0;
         }
-        for (int i = 0; i < kCodeStages; ++i) {
-            mbar_init(&sh.code_full[i], 1);
-            mbar_init(&sh.code_empty[i], 128);
-        }
+        mbar_init(&sh.vmax_ready, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], kRows + 1);
@@ -165,7 +167,6 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         mbar_init(&sh.drained, 1);
         sh.any_bad = 0;
         sh.failed = 0;
-        sh.vmax = 0;
         fence_barrier_init();
     }
     if (warp == MMA) tmem_alloc(&sh.tmem, TMEM);
@@ -184,17 +185,13 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         return false;
     };
     // registers go to the softmax warps, within what the block was launched with:
-    // 256 x 208 + 128 x 88 = 384 x 168, 256 x 184 + 128 x 56 + 128 x 88 = 512 x 128,
-    // 128 x 184 + 128 x 72 = 256 x 128
+    // 256 x 208 + 128 x 88 = 384 x 168, 128 x 184 + 128 x 72 = 256 x 128
     if (warp < MMA) {
-        if constexpr (FP8 || NQ == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    } else if (FP8 && warp < CONVERT) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    } else if (NQ == 1) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
 
     if (warp < MMA) {
@@ -207,7 +204,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const int first = s.first + t0 + i * per, last = s.first + min(s.n, t0 + (i + 1) * per) - 1;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor memory lane of this warp, bits 16 up
         const uint32_t sa = tmem + lanes + S_COL[i], oa = tmem + lanes + O_COL[i];
-        float m = live ? -INFINITY : 0.f, l = 0.f;
+        float m = live ? -INFINITY : 0.f, l = 0.f, vscale = 1.f;
         bool ok = true;
         // Key tiles [whole0, whole1) are seen as a whole by every row of the row tile:
         // full tiles of window pages up to the first row's position (tiles of sinks
@@ -220,7 +217,11 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             whole1 = (pages.head + max((first + 1) / p.P - pages.body0, 0)) / ppt;
         }
         bool unset = true;                    // a row of the warp has seen nothing yet
-        for (int j = 0; j < tiles[i]; ++j) {
+        if constexpr (SCALED) {
+            ok = tiles[i] == 0 || wait(&sh.vmax_ready, 0);
+            if (ok && tiles[i] > 0) vscale = sh.vmax > 0.f ? 1.f / sh.vmax : 0.f;
+        }
+        for (int j = 0; ok && j < tiles[i]; ++j) {
             if (!wait(&sh.s_full[i], j & 1)) { ok = false; break; }
             tc_fence_after();
             uint32_t x[kKeys];
@@ -228,10 +229,8 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             const bool bad = *(volatile int *)&sh.any_bad != 0;
             const bool masked = bad || j < whole0 || j >= whole1;
             while (true) {
-                tmem_ld32(sa, x);
-                tmem_ld32(sa + 32, x + 32);
-                tmem_ld32(sa + 64, x + 64);
-                tmem_ld32(sa + 96, x + 96);
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(sa + c, x + c);
                 tmem_wait_ld();
                 if (masked) {
 #pragma unroll
@@ -255,40 +254,34 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         for (int e = 0; e < 4; ++e)
                             t[e] = fmaxf(fmaxf(__uint_as_float(x[q * 16 + e]), __uint_as_float(x[q * 16 + 4 + e])),
                                          fmaxf(__uint_as_float(x[q * 16 + 8 + e]), __uint_as_float(x[q * 16 + 12 + e])));
-                        top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (FP8 ? sh.ks[j % kScaleRing][q] : 1.f));
+                        top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) *
+                                             (SCALED ? sh.ks[j % kScaleRing][q] : 1.f));
                     }
                     const float m_new = fmaxf(m, top * p.scale_log2);
                     const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
                     m = m_new;
                     l *= f;
                     if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) { // the last product into O is complete: S of this tile follows it
-                            uint32_t o[32];
-                            tmem_ld32(oa + c, o);
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) { // the last product into O is complete: S of this tile follows it
+                            uint32_t o[16];
+                            tmem_ld16(oa + c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(oa + c, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(oa + c, o);
                         }
                         tmem_wait_st();
                     }
                     unset = __any_sync(0xffffffffu, m == -INFINITY);
-                    raise = false;
                     raised = true;
-                    continue;                             // the scores' registers were needed
                 }
                 const float base = m == -INFINITY ? 0.f : m;
                 float2 sum[4] = {};
-                float vscale = 1.f;
-                if constexpr (FP8) {
-                    const float top = __uint_as_float(*(volatile uint32_t *)&sh.vmax);
-                    vscale = top > 0.f ? 1.f / top : 0.f;
-                }
 #pragma unroll
                 for (int q = 0; q < kKeys / 16; ++q) {
                     float vs = 1.f, scale = p.scale_log2;
-                    if constexpr (FP8) {
+                    if constexpr (SCALED) {
                         vs = sh.vamax[j % kScaleRing][q] * vscale;
                         scale *= sh.ks[j % kScaleRing][q];
                     }
@@ -300,7 +293,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         w.y = exp2_fast(w.y);
                         sum[c / 2 & 3] = add2(sum[c / 2 & 3], w);
                         // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
-                        x[e / 2] = FP8 ? mma16816<T>::pack2(w.x * vs, w.y * vs) : mma16816<T>::pack2(w.x, w.y);
+                        x[e / 2] = SCALED ? mma16816<T>::pack2(w.x * vs, w.y * vs) : mma16816<T>::pack2(w.x, w.y);
                     }
                 }
                 sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
@@ -311,8 +304,8 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 }
                 raise = true;
             }
-            tmem_st32(sa, x);
-            tmem_st32(sa + 32, x + 32);
+#pragma unroll
+            for (int c = 0; c < kKeys / 2; c += 32) tmem_st32(sa + c, x + c);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&sh.p_full[i]);
@@ -323,8 +316,8 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         if (ok) {
             float inv = l > 0.f ? 1.f / l : 0.f;      // a row that sees nothing is zero
-            if constexpr (FP8) inv *= fp8_scale(__uint_as_float(*(volatile uint32_t *)&sh.vmax));
-            T *dst = static_cast<T *>(p.out) + (((size_t)b * p.T + tok) * p.Hq + h * p.G + g) * D;
+            if constexpr (SCALED) inv *= tiles[i] > 0 ? fp8_scale(sh.vmax) : 0.f;
+            T *dst = static_cast<T *>(p.out) + (((size_t)seq * p.T + tok) * p.Hq + h * p.G + g) * D;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -410,78 +403,86 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         __syncwarp();
     } else if (warp == LOAD) {
         // -------------------------------------------------------- pages by TMA
-        // A lane brings one box of a tile: block lane % NB of page lane / NB, or
-        // the codes of page `lane`.
-        constexpr int BOXES = FP8 ? 1 : NB;
-        uint64_t *full = FP8 ? sh.code_full : sh.kv_full, *empty = FP8 ? sh.code_empty : sh.kv_empty;
-        constexpr int STAGES = FP8 ? kCodeStages : NS;
+        // A lane brings one box of a tile: block lane % NB of page lane / NB.
         if (lane == 0) {
             prefetch_tensormap(&qmap);
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);
         }
-        if (n > 0) {
-            if (lane == 0) {
-                const int q_tiles = tiles[1] > 0 ? 2 : 1;       // the first tile has rows; its keys may all be hidden
-                mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_tiles * NB * per * p.G * 128));
-                for (int i = 0; i < q_tiles; ++i)
-                    for (int c = 0; c < NB; ++c)
-                        tma_load_3d(qtile + (i * NB + c) * BLOCK, &qmap, &sh.q_full, c * 64, h * p.G,
-                                    b * p.T + t0 + i * per);
+        if (n > 0 && lane == 0) {
+            const int q_tiles = tiles[1] > 0 ? 2 : 1;           // the first tile has rows; its keys may all be hidden
+            mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_tiles * NB * per * p.G * 128));
+            for (int i = 0; i < q_tiles; ++i)
+                for (int c = 0; c < NB; ++c)
+                    tma_load_3d(qtile + (i * NB + c) * BLOCK, &qmap, &sh.q_full, c * 64, h * p.G, seq * p.T + t0 + i * per);
+        }
+        // E4M3: the pages of the whole call lie one after the other in the workspace
+        Pages call{};
+        if constexpr (SCALED) call = visible_pages(s.first, s.first + s.n - 1, p.window, p.sinks, p.P);
+        float2 amax = make_float2(0.f, 0.f);                    // of the lane's page
+        auto look_up = [&](int j) {                             // its first pool row, or -1
+            const int k = j * ppt + lane / NB;
+            if (lane >= ppt * NB || j >= n || k >= pages.count) return -1;
+            const int pg = pages.page(k), phys = table[pg];
+            if (phys >= 0 && phys < p.num_phys) {
+                if constexpr (SCALED) {
+                    amax = *reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4);
+                    const int at = pg < call.head ? pg : call.head + pg - call.body0;
+                    return ((b * p.ws_pages + at) * p.Hkv + h) * p.P;
+                }
+                return (phys * p.Hkv + h) * p.P;
             }
-            float2 amax = make_float2(0.f, 0.f);
-            auto look_up = [&](int j) {
-                const int k = j * ppt + lane / BOXES;
-                if (lane >= ppt * BOXES || j >= n || k >= pages.count) return -1;
-                const int phys = table[pages.page(k)];
-                if (phys >= 0 && phys < p.num_phys) {
-                    if constexpr (FP8) amax = *reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + h) * 4);
-                    return phys;
+            *(volatile int *)&sh.any_bad = 1;
+            if (p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
+            return -1;
+        };
+        int row = look_up(0);
+        bool ok = true;
+        for (int j = 0; ok && j < n; ++j) {
+            if constexpr (SCALED) {
+                // a page without keys has the scale 0, under which a hidden score's -inf would be NaN
+                const int pg = lane / NB;
+                for (int q = pg * p.P / 16; lane % NB == 0 && pg < ppt && q < (pg + 1) * p.P / 16; ++q) {
+                    sh.ks[j % kScaleRing][q] = row >= 0 ? fmaxf(fp8_scale(amax.x), 1e-30f) : 1.f;
+                    sh.vamax[j % kScaleRing][q] = row >= 0 ? amax.y : 0.f;
                 }
-                *(volatile int *)&sh.any_bad = 1;
-                if (p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
-                return -1;
-            };
-            int phys = look_up(0), issued = 0;
-            bool ok = true;
-            for (int j = 0; ok && j < n; ++j) {
-                if constexpr (FP8) {
-                    // a page without keys has the scale 0, under which a hidden score's -inf would be NaN
-                    for (int q = lane * p.P / 16; lane < ppt && q < (lane + 1) * p.P / 16; ++q) {
-                        sh.ks[j % kScaleRing][q] = phys >= 0 ? fmaxf(fp8_scale(amax.x), 1e-30f) : 1.f;
-                        sh.vamax[j % kScaleRing][q] = phys >= 0 ? amax.y : 0.f;
-                    }
-                }
-                const int next = look_up(j + 1);
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, phys >= 0)) * p.P * (FP8 ? D : 128);
-                for (int v = 0; v < 2; ++v) {
-                    const int at = 2 * j + v, st = at % STAGES;
-                    ok = at < STAGES || wait(&empty[st], (at / STAGES - 1) & 1);
-                    if (!ok) break;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
-                    __syncwarp();
-                    if (phys >= 0) {
-                        const int row = (phys * p.Hkv + h) * p.P;
-                        if constexpr (FP8)
-                            tma_load_2d(codes + st * kKeys * D + lane * p.P * D, v ? &vmap : &kmap, &full[st], 0, row);
-                        else
-                            tma_load_2d(ring + st * kv_bytes<D>() + (lane % NB) * BLOCK + (lane / NB) * p.P * 128,
-                                        v ? &vmap : &kmap, &full[st], (lane % NB) * 64, row);
-                    }
-                    issued = at + 1;
-                }
-                phys = next;
             }
-            // every copy has landed before the CTA may end
-            if (!mbar_wait_bounded(&sh.q_full, 0, p.drain_limit_ns)) give_up();
-            for (int at = max(0, issued - STAGES); at < issued; ++at)
-                if (!mbar_wait_bounded(&full[at % STAGES], at / STAGES & 1, p.drain_limit_ns)) give_up();
+            const int next = look_up(j + 1);
+            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0)) * p.P * 128;
+            for (int v = 0; v < 2; ++v) {
+                const int at = 2 * j + v, st = at % NS;
+                ok = at < NS || wait(&sh.kv_empty[st], (at / NS - 1) & 1);
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) {
+                    sh.armed[st] = at / NS + 1;
+                    mbar_arrive_expect_tx(&sh.kv_full[st], bytes);
+                }
+                __syncwarp();
+                if (row >= 0)
+                    tma_load_2d(ring + st * kv_bytes<D>() + (lane % NB) * BLOCK + (lane / NB) * p.P * 128, v ? &vmap : &kmap,
+                                &sh.kv_full[st], (lane % NB) * 64, row);
+            }
+            row = next;
+        }
+    } else if (SCALED && warp == LARGEST) {
+        // Weights carry the values' scales as a share of the largest one, so that
+        // small scales lose nothing in 16 bits.
+        float top = 0.f;
+        for (int k = lane; k < pages.count; k += 32) {
+            const int pg = pages.page(k);
+            if (good_page(p, table, pg)) top = fmaxf(top, p.scales[((size_t)table[pg] * p.Hkv + h) * 4 + 1]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) {
+            sh.vmax = top;
+            mbar_arrive(&sh.vmax_ready);
         }
     } else if (warp == KEEP) {
         // --------------------------------------------------- tiles looked after
         // Values that no row sees may be anything, and 0 * NaN is not 0: such rows
-        // become zeros (E4M3: when they are converted).  Only the last page, the
+        // become zeros.  Only the last page, the
         // pages where the sinks end and the window begins, and tiles with bad or no
         // pages have them.
         bool ok = true;
@@ -491,7 +492,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (!ok) break;
             const bool bad = *(volatile int *)&sh.any_bad != 0;
             const int k0 = j * ppt, k1 = k0 + ppt;
-            if (!FP8 && (bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head))) {
+            if ((bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head))) {
                 for (int r = lane; r < kKeys; r += 32) {
                     const int k = k0 + r / p.P, pg = pages.page(k), at = pg * p.P + r % p.P;
                     const bool seen = k < pages.count && at <= pages.hi && (at >= pages.lo || at < p.sinks) &&
@@ -514,94 +515,75 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 if (ok && lane == 0) mbar_arrive(&sh.p_full[i]);
             }
         }
-    } else if (FP8 && warp >= CONVERT) {
-        // --------------------------------------------- E4M3 codes to f16 tiles
-        // Codes are exact in f16; the keys' scale multiplies the scores and the
-        // values' scale the weights, as a share of the largest one (vmax), so that
-        // small scales lose nothing in 16 bits.
-        constexpr int CPR = D / 16, RPI = 32 / CPR, IT = 32 / RPI;   // chunks per row, rows per step, steps
-        const int cw = warp - CONVERT, chunk = lane % CPR, rsub = lane / CPR;
-        float top = 0.f;
-        for (int k = tid - 32 * CONVERT; k < pages.count; k += 128) {
-            const int pg = pages.page(k);
-            if (good_page(p, table, pg)) top = fmaxf(top, p.scales[((size_t)table[pg] * p.Hkv + h) * 4 + 1]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) atomicMax(&sh.vmax, __float_as_uint(top));
-        named_barrier_sync(1, 128);
-        bool ok = true;
-        for (int at = 0; ok && at < 2 * n; ++at) {
-            const int v = at & 1, j = at >> 1, cs = at % kCodeStages, st = at % NS;
-            ok = wait(&sh.code_full[cs], at / kCodeStages & 1);
-            if (!ok) break;
-            uint4 w[IT];
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int r = cw * 32 + it * RPI + rsub;
-                // 128-byte rows are swizzled
-                w[it] = *reinterpret_cast<const uint4 *>(codes + cs * kKeys * D + r * D +
-                                                         ((D == 128 ? chunk ^ (r & 7) : chunk) << 4));
-            }
-            if (v) {
-                const bool bad = *(volatile int *)&sh.any_bad != 0;
-                const int k0 = j * ppt, k1 = k0 + ppt;
-                if (bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head)) {
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {                // as above: values that no row sees become zeros
-                        const int r = cw * 32 + it * RPI + rsub;
-                        const int k = k0 + r / p.P, pg = pages.page(k), tok = pg * p.P + r % p.P;
-                        const bool seen = k < pages.count && tok <= pages.hi && (tok >= pages.lo || tok < p.sinks) &&
-                                          (!bad || good_page(p, table, pg));
-                        if (!seen) w[it] = make_uint4(0, 0, 0, 0);
-                    }
-                }
-            }
-            ok = at < NS || wait(&sh.kv_empty[st], (at / NS - 1) & 1);
-            if (!ok) break;
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int r = cw * 32 + it * RPI + rsub;
-                uint4 a, c;
-                codes_to_h(w[it].x, &a.x);
-                codes_to_h(w[it].y, &a.z);
-                codes_to_h(w[it].z, &c.x);
-                codes_to_h(w[it].w, &c.z);
-                unsigned char *row = ring + st * kv_bytes<D>() + (chunk / 4) * BLOCK + r * 128;
-                *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2) ^ (r & 7)) << 4)) = a;
-                *reinterpret_cast<uint4 *>(row + (((chunk % 4 * 2 + 1) ^ (r & 7)) << 4)) = c;
-            }
-            // The codes go back only here: an arrival right after the loads overtakes
-            // them, and the next copy then lands before they have read.
-            mbar_arrive(&sh.code_empty[cs]);
-            fence_async_smem();
-            mbar_arrive(&sh.kv_full[st]);
-        }
     }
     tc_fence_before();
     __syncthreads();
+    // Every copy has been waited for by the warps that used it, unless some wait gave
+    // up: no copy may land after the CTA's end.
+    if (tid == 0 && *(volatile int *)&sh.failed) {
+        if (n > 0) (void)mbar_wait_bounded(&sh.q_full, 0, p.drain_limit_ns);
+        for (int st = 0; st < NS; ++st)
+            if (sh.armed[st] > 0) (void)mbar_wait_bounded(&sh.kv_full[st], (sh.armed[st] - 1) & 1, p.drain_limit_ns);
+    }
     if (warp == MMA) {
         tc_fence_after();
         tmem_free(tmem, TMEM);
     }
 }
 
-template <typename T, bool FP8, int D>
+// The codes of the pages that some query of the call sees, as halves, page after page
+// of a sequence: [batch][ws_pages][Hkv][P][d], keys then values.  One block of 256
+// threads per (page, sequence); bound by the 5 bytes read and written per code pair.
+__global__ void __launch_bounds__(256) unpack_codes_kernel(WindowParams p, int d, __half *keys, __half *values) {
+    const int b = blockIdx.y, seq = p.b0 + b;
+    const QuerySpan s = query_span(p, seq, false);
+    if (s.n <= 0) return;
+    const Pages call = visible_pages(s.first, s.first + s.n - 1, p.window, p.sinks, p.P);
+    const int k = blockIdx.x;
+    if (k >= call.count) return;
+    const int phys = p.block_table[(size_t)seq * p.max_pages + call.page(k)];
+    if (phys < 0 || phys >= p.num_phys) return;                 // reported where it is looked up for its use
+    const size_t page = (size_t)p.Hkv * p.P * d;                // codes of a page
+    const size_t from = phys * page, to = ((size_t)b * p.ws_pages + k) * page;
+    const uint4 *src[2] = {reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.k_pool) + from),
+                           reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.v_pool) + from)};
+    __half *dst[2] = {keys + to, values + to};
+#pragma unroll 2
+    for (int x = threadIdx.x; x < (int)(page / 8); x += 256) {  // keys, then values
+        const int v = x >= (int)(page / 16), at = x - v * (int)(page / 16);
+        const uint4 c = ld_global_nc_v4(src[v] + at);
+        uint4 lo, hi;
+        codes_to_h(c.x, &lo.x);
+        codes_to_h(c.y, &lo.z);
+        codes_to_h(c.z, &hi.x);
+        codes_to_h(c.w, &hi.z);
+        reinterpret_cast<uint4 *>(dst[v])[2 * at] = lo;
+        reinterpret_cast<uint4 *>(dst[v])[2 * at + 1] = hi;
+    }
+}
+
+template <typename T, bool SCALED, int D>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, WindowParams p, cudaStream_t stream) {
-    constexpr int NQ = !FP8 && D == 64 ? 1 : 2;
-    auto kernel = window_prompt_kernel<T, FP8, D, NQ>;
-    constexpr size_t smem = prompt_smem<D, FP8, NQ>();
+    constexpr int NQ = D == 64 ? 1 : 2;
+    auto kernel = window_prompt_kernel<T, SCALED, D, NQ>;
+    constexpr size_t smem = prompt_smem<D, NQ>();
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int per = NQ * (kRows / p.G);
     p.row_tiles = (p.T + per - 1) / per;
     const long long blocks = (long long)p.row_tiles * p.B * p.Hkv;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kernel<<<(unsigned)blocks, prompt_threads<FP8, NQ>(), smem, stream>>>(q, k, v, p);
+    kernel<<<(unsigned)blocks, prompt_threads<NQ>(), smem, stream>>>(q, k, v, p);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t launch_unpack_codes(int D, const WindowParams &p, void *keys, void *values, cudaStream_t stream) {
+    unpack_codes_kernel<<<dim3(p.ws_pages, p.B), 256, 0, stream>>>(p, D, static_cast<__half *>(keys),
+                                                                   static_cast<__half *>(values));
+    return cudaGetLastError();
+}
 
 cudaError_t launch_window_prompt(qasa_dtype dt, int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                  const WindowParams &p, cudaStream_t stream) {
