@@ -315,7 +315,10 @@ qasa_status qasa_dense_decode_attention(const qasa_kv_cache *cache, const void *
  *   window         >= 1, the query's own token included
  *   sink_tokens    >= 0
  *   workspace      device memory of qasa_window_workspace_size bytes, 16-byte
- *                  aligned (scratch, no initialisation; NULL where that is 0)
+ *                  aligned (scratch, no initialisation; NULL where that is 0: it is
+ *                  only prompts over an E4M3 cache, more than 128 query rows per KV
+ *                  head, that need any, for the visible pages as halves; at most
+ *                  512 MiB, or one sequence's)
  * Any group size 1..8, max_q_tokens up to 65536.  Pages that hold no token that
  * some query of the sequence sees are not read, and neither are their block-table
  * entries: a rolling cache may have given them back.  Keys and values of tokens

@@ -604,8 +604,9 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     p.P = cache->page_size;
     p.max_pages = max_pages_per_seq;
     p.num_phys = cache->num_phys_pages;
-    p.window = window;
-    p.sinks = sink_tokens;
+    // no position reaches 2^30, and differences with these stay inside 32 bits
+    p.window = window < 1 << 30 ? window : 1 << 30;
+    p.sinks = sink_tokens < 1 << 30 ? sink_tokens : 1 << 30;
     const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)cache->head_dim);
     p.scale_log2 = (float)(sc * 1.4426950408889634);
     p.row_tiles = 1;

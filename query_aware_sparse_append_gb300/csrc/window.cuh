@@ -53,6 +53,16 @@ __device__ __forceinline__ bool sees(int i, int j, int window, int sinks) {
     return j <= i && (j < sinks || j > i - window);
 }
 
+// Weights are exp2(score - m) with m this far below the largest score (log2 units),
+// which the sums and outputs carry too, so that it cancels.  fp16 weights of the
+// largest scores are then 2^7, and only those 2^-21 times as large fall below its
+// normal numbers, where a rounding is no longer relative: values under a large E4M3
+// scale may still count for something there.  bf16 has fp32's range.
+template <typename T> constexpr float kHeadroom = elem<T>::id == QASA_DTYPE_F16 ? 7.f : 0.f;
+// Sum of the weights that one pass gives a row from which on it looks for its own
+// maximum: every single weight is inside fp16 up to there.
+constexpr float kMostWeight = 32768.f;
+
 // First pool row (token slot) of tile `t` for KV head h, or -1 for a bad page.
 __device__ __forceinline__ long long tile_row(const WindowParams &p, const int32_t *table, int t, int h, int &phys) {
     const int per_page = p.P / kTile;

@@ -28,9 +28,9 @@
 //
 // No maximum is sought where it is not needed: a tile's weights are taken against
 // the maximum so far, and only where a row's weights of the tile then sum to more
-// than 2^12 is the tile's own maximum found, O and the sum rescaled and the tile
-// done again.  Up to there nothing is lost: the sums are fp32, and 16-bit weights
-// keep their relative half step up to 2^12 as well as below 1.
+// than kMostWeight is the tile's own maximum found, O and the sum rescaled and the
+// tile done again.  Up to there nothing is lost: the sums are fp32, and 16-bit
+// weights keep their relative half step whatever their size (window.cuh).
 //
 // E4M3 caches: a kernel before this one writes the codes of the pages in question as
 // halves, which they are exactly (converting them here, once per 256 rows, kept the
@@ -45,7 +45,6 @@ namespace {
 
 constexpr int kRows = 128;            // rows of a row tile
 constexpr int kKeys = 128;            // tokens of a key tile
-constexpr float kMostWeight = 4096.f; // sum of a tile's weights from which on its maximum is sought
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
@@ -257,7 +256,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) *
                                              (SCALED ? sh.ks[j % kScaleRing][q] : 1.f));
                     }
-                    const float m_new = fmaxf(m, top * p.scale_log2);
+                    const float m_new = fmaxf(m, top * p.scale_log2 - kHeadroom<T>);
                     const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
                     m = m_new;
                     l *= f;

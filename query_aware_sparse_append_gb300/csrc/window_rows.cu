@@ -122,7 +122,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 }
 
 constexpr int kSlots = 3;                      // copies under way per warp: keys, values, the next keys
-constexpr float kMostWeight = 4096.f;          // sum of a step's weights from which on its maximum is sought
 
 // What a warp takes at once: `TPS` tiles, so that a copy is 4 KB (2 KB: E4M3, d 64).
 template <bool FP8, int D> struct Step {
@@ -381,7 +380,7 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float m_new = fmaxf(m[x][e], top);
+                        const float m_new = fmaxf(m[x][e], top - kHeadroom<T>);
                         f[e] = m_new == -INFINITY ? 1.f : exp2_fast(m[x][e] - m_new);
                         m[x][e] = m_new;
                         l[x][e] *= f[e];

@@ -236,3 +236,94 @@ def test_prompt_waits_with_a_short_limit_end_or_are_reported(dtype, monkeypatch)
     monkeypatch.delenv("QASA_WAIT_LIMIT_NS")
     out = _run(c, q, [300, 300], 200, 4, 300)
     _check(c, q, out, [300, 300], 200, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "e4m3", "f32"])
+@pytest.mark.parametrize("tiles", [3, 9, 17, 25, 33, 41, 49, 57, 65, 130])
+def test_every_number_of_ctas_to_a_unit(dtype, tiles):
+    # one KV head, one sequence: the number of CTAs follows the visible tiles of 16 tokens
+    L = 16 * tiles - 5
+    c = R.Paged(dtype, [L], 1, 64, 16, seed=21)
+    c.table = c.table[:, :-(-L // 16)].contiguous()
+    q = _queries(c, 1, 4)
+    out = _run(c, q, [1], None, 0, 1)
+    _check(c, q, out, [1], None, 0)
+
+
+@pytest.mark.parametrize("T,group", [(70, 2), (33, 4), (128, 1), (65, 2)])
+def test_prompt_kernel_and_few_rows_kernel_meet_on_e4m3(T, group):
+    # up to 128 query rows the pages are read as they are, from there on unpacked first
+    c = R.Paged("e4m3", [T + 300, T], 2, 128, 32, seed=22, amax_spread=2.0)
+    q = _queries(c, T, 2 * group)
+    for window, sinks in ((None, 0), (100, 35)):
+        out = _run(c, q, [T, T], window, sinks, T)
+        _check(c, q, out, [T, T], window, sinks)
+
+
+def test_e4m3_prompts_in_several_groups_of_sequences():
+    # a table of 16384 pages: half a GiB holds the pages of eight sequences, nine are asked for
+    qasa = _qasa()
+    lens = [200 + 17 * b for b in range(9)]
+    c = R.Paged("e4m3", lens, 1, 64, 16, seed=23)
+    wide = torch.full((9, 16384), R.BAD_PAGE, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    n = [200 - b for b in range(9)]
+    q = _queries(c, 200, 1)
+    cache = c.library()
+    bytes_ = qasa.alloc_window_workspace(cache, 9, 1, 200, 16384).numel()
+    assert bytes_ == 8 * 16384 * 16 * 64 * 4
+    out = _run(c, q, n, None, 0, 200)
+    for b, L in enumerate(lens):
+        ref, weighed, size = R.attention(c, q[b], b, L, n[b], None, 0)
+        assert bool(((out[b, :n[b]].double() - ref).abs() <= R.attention_tolerance(ref, weighed, size, 64, torch.float16)).all()), b
+
+
+def test_too_small_a_workspace_is_refused():
+    qasa = _qasa()
+    c = R.Paged("e4m3", [400], 1, 64, 16, seed=24)
+    q = _queries(c, 200, 1)
+    with pytest.raises(qasa.QasaError, match="workspace"):
+        qasa.window_attention(c.library(), q, c.table, c.seq_lens, workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,T", [("f16", 1), ("f16", 40), ("e4m3", 1), ("e4m3", 200), ("f32", 3)])
+def test_pages_beyond_four_gib(dtype, T):
+    # the same pages at the far end of pools whose last byte is beyond 2^32
+    qasa = _qasa()
+    c = R.Paged(dtype, [300 + T], 1, 128, 16, seed=25)
+    es = c.k_pool.element_size()
+    far = (5 << 30) // (16 * 128 * es)
+    kv = torch.empty((2, far, 1, 16, 128), dtype=c.k_pool.dtype, device="cuda")
+    kv[0, far - c.count:], kv[1, far - c.count:] = c.k_pool, c.v_pool
+    bounds = torch.empty((far, 1, 2, 128), dtype=c.k_pool.dtype, device="cuda")
+    scales = torch.empty((far, 1, 4), device="cuda") if dtype == "e4m3" else None
+    if scales is not None:
+        scales[far - c.count:] = c.scales
+    table = torch.where(c.table < c.count, c.table + (far - c.count), c.table)
+    q = _queries(c, T, 4)
+    near = qasa.window_attention(c.library(), q, c.table, c.seq_lens, 250, 4)
+    there = qasa.window_attention(qasa.PagedKVCache(kv[0], kv[1], bounds, scales), q, table, c.seq_lens, 250, 4)
+    assert torch.equal(near, there)
+    _check(c, q, there, [T], 250, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "e4m3"])
+def test_two_calls_at_once_on_two_streams(dtype):
+    qasa = _qasa()
+    c = R.Paged(dtype, [600, 300], 2, 128, 16, seed=26)
+    cache = c.library()
+    qs = [_queries(c, T, 8, seed=T) for T in (1, 150, 1, 150)]
+    alone = [qasa.window_attention(cache, q, c.table, c.seq_lens, 200, 4) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    outs = [torch.zeros_like(q) for q in qs]
+    for _ in range(3):
+        for q, out, s in zip(qs, outs, streams):
+            with torch.cuda.stream(s):
+                qasa.window_attention(cache, q, c.table, c.seq_lens, 200, 4, out=out)
+        for q, out, s in zip(qs, outs, streams):      # the stream named in the call
+            qasa.window_attention(cache, q, c.table, c.seq_lens, 200, 4, out=out, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, outs):
+        assert torch.equal(a, b)
