@@ -51,6 +51,9 @@ class _TokenRows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
+_ThreeRows = ctypes.c_int64 * 9      # three qasa_token_rows, filled at once
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _C = ctypes.POINTER(_Cache)
@@ -73,8 +76,7 @@ _lib.qasa_dense_decode_attention.restype = _I
 _lib.qasa_sparse_decode_attention_noalloc.argtypes = [_C, _P, _I, _P, _I, _P, _P, _I, ctypes.c_float,
                                                       _P, _P, _P, _I, _P, _P]
 _lib.qasa_sparse_decode_attention_noalloc.restype = _I
-_R = ctypes.POINTER(_TokenRows)
-_lib.qasa_kv_append_rotated.argtypes = [_C, ctypes.POINTER(_Rotation), _P, _I, _P, _P, _R, _I, _P, _R, _R, _I, _I, _P, _P]
+_lib.qasa_kv_append_rotated.argtypes = [_C, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _I, _P, _P]
 _lib.qasa_kv_append_rotated.restype = _I
 _lib.qasa_window_workspace_size.argtypes = [_I, _I, _C, _I, _I, _I, _I]
 _lib.qasa_window_workspace_size.restype = ctypes.c_size_t
@@ -269,13 +271,14 @@ def _status_arg(status: Optional[torch.Tensor], index: int):
     raise ValueError("status must be an int32 tensor on cuda:%d" % index)
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, head_dim: int, index: int) -> _TokenRows:
+def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, head_dim: int, index: int) -> tuple:
+    """The fields of a qasa_token_rows."""
     if t.dim() != 4 or t.dtype is not dtype or t.get_device() != index:
         raise ValueError("%s must be a %s tensor [batch, tokens, heads, head_dim] on cuda:%d" % (name, dtype, index))
     sb, st, sh, sc = t.stride()
     if (sc != 1 or sh != head_dim) and t.numel() and (sc != 1 or t.shape[2] > 1):
         raise ValueError("the heads of a token of %s must be contiguous" % name)
-    return _TokenRows(t.data_ptr(), sb, st)
+    return t.data_ptr(), sb, st
 
 
 def _call_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
@@ -326,9 +329,9 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
         raise ValueError("table must be [max_positions, 2, rot_dim / 2]")
     positions, _, half = angles = table.shape
     rot = _Rotation(_arg(table, "table", torch.float32, angles, index), positions, 2 * half, 1 if interleaved else 0)
-    qr, hq, out = None, 0, None
+    qr, hq, out = (0, 0, 0), 0, None
     if q is not None:
-        qr = ctypes.byref(_token_rows(q, "q", value, d, index))
+        qr = _token_rows(q, "q", value, d, index)
         qb, qt, hq, qd = q.shape
         if qb != B or qt != T or qd != d:
             raise ValueError("q must have the batch and tokens of k_new and the cache's head_dim")
@@ -339,10 +342,12 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
         raise ValueError("q_out without q")
     if index < 0:
         raise ValueError("the cache must be on a CUDA device")
+    rows = _ThreeRows(*kr, *vr, *qr)
+    at = ctypes.addressof(rows)
     code = _lib.qasa_kv_append_rotated(
         cache.c_ref, ctypes.byref(rot), _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
         _arg(seq_lens, "seq_lens", torch.int32, (B,), index), _arg(append_lens, "append_lens", torch.int32, (B,), index),
-        qr, hq, out, ctypes.byref(kr), ctypes.byref(vr), B, T, _status_arg(status, index), _call_stream(stream, index))
+        None if q is None else at + 48, hq, out, at, at + 24, B, T, _status_arg(status, index), _call_stream(stream, index))
     if code:
         _check(code, "qasa_kv_append_rotated")
     return q_out
@@ -351,11 +356,16 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
 NO_WINDOW = 0x7FFFFFFF      # a window that every token is in
 
 
+def _tokens(n: Optional[int]) -> int:
+    """A count of tokens as the library takes it (None: all)."""
+    return NO_WINDOW if n is None else min(int(n), NO_WINDOW)
+
+
 def alloc_window_workspace(cache: PagedKVCache, batch: int, num_q_heads: int, max_q_tokens: int,
                            max_pages_per_seq: int, window: Optional[int] = None, sink_tokens: int = 0) -> torch.Tensor:
     """Workspace of window_attention calls of up to this shape with this window."""
     n = int(_lib.qasa_window_workspace_size(batch, num_q_heads, cache.c_ref, max_q_tokens, max_pages_per_seq,
-                                            NO_WINDOW if window is None else int(window), sink_tokens))
+                                            _tokens(window), _tokens(sink_tokens)))
     return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_pool.device)
 
 
@@ -399,7 +409,7 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
     code = _lib.qasa_window_attention(
         cache.c_ref, qp, hq, T, _arg(q_lens, "q_lens", torch.int32, (B,), index),
         _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
-        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), NO_WINDOW if window is None else window, sink_tokens,
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), _tokens(window), _tokens(sink_tokens),
         scale or 0.0, _arg(out, "out", value, shape, index), workspace.data_ptr(), workspace.nbytes, B,
         _status_arg(status, index), _call_stream(stream, index))
     if code:

@@ -440,11 +440,11 @@ long long most_visible_tiles(int max_pages, int P, int T, int window, int sinks)
 }
 
 // CTAs per unit of the few-rows kernel: what fills the SMs with four CTAs each, so
-// that all run at once, as long as every warp has two tiles or so: with few units
+// that all run at once, as long as every warp has a tile: with few units
 // the chain of a warp's tiles is what a call takes.
 int window_cluster(long long units, long long tiles) {
     const int sms = sm_count() > 0 ? sm_count() : 152;
-    const long long fill = 4LL * sms / (units > 0 ? units : 1), work = tiles / 8;
+    const long long fill = 4LL * sms / (units > 0 ? units : 1), work = tiles / 4;
     const long long c = fill < work ? fill : work;
     return c < 1 ? 1 : c > 8 ? 8 : (int)c;
 }
