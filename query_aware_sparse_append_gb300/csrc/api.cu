@@ -615,6 +615,8 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     p.drain_limit_ns = kWaitLimitNs;
     p.b0 = 0;
     p.ws_pages = 0;
+    p.sms = sm_count() > 0 ? sm_count() : 1;
+    p.most_tiles = most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens);
     if (!window_few_rows(cache->dtype, (long long)p.T * p.G)) {
         CUtensorMap qm, km, vm;
         st = query_tensor_map(&qm, q, cache->dtype, cache->head_dim, num_q_heads, p.G, (long long)batch * p.T);

@@ -59,6 +59,8 @@ struct WindowParams {
     float scale_log2;
     int cluster;         // CTAs that share a unit (row tile of a sequence and KV head)
     int row_tiles;       // row tiles (pairs of them in the prompt kernel) of the longest sequence
+    int sms;             // prompt kernel: SMs of the device
+    long long most_tiles;   // prompt kernel: the most 16-token tiles that a CTA's rows see
     int b0;              // prompt kernel: first sequence of the launch, which has B of them
     int ws_pages;        // E4M3, prompt kernel: pages per sequence in the workspace
     unsigned long long wait_limit_ns;    // prompt kernel: waits on other warps

@@ -26,6 +26,11 @@
 //              issuing thread's place: the barrier of the weights takes its arrival too
 // Tensor memory: S0, S1 (P over them), O0, O1.
 //
+// Where a call has fewer CTAs than the SMs hold (a few drafted tokens of a few
+// sequences), a cluster shares a CTA's rows: each takes a stretch of the key tiles,
+// and the partial outputs are joined through distributed shared memory, always in
+// the same order.
+//
 // No maximum is sought where it is not needed: a tile's weights are taken against
 // the maximum so far, and only where a row's weights of the tile then sum to more
 // than kMostWeight is the tile's own maximum found, O and the sum rescaled and the
@@ -45,6 +50,7 @@ namespace {
 
 constexpr int kRows = 128;            // rows of a row tile
 constexpr int kKeys = 128;            // tokens of a key tile
+constexpr int kMostJoined = 8;        // CTAs that share the key tiles of their rows
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
@@ -109,8 +115,10 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 // products.
 template <int NQ> constexpr int prompt_threads() { return NQ * 128 + 128; }
 
-// T: 16-bit type of q, out and the pages; SCALED: pages of E4M3 values (as halves).
-template <typename T, bool SCALED, int D, int NQ>
+// T: 16-bit type of q, out and the pages; SCALED: pages of E4M3 values (as halves);
+// JOIN: a cluster shares the key tiles (apart, as the other form's softmax is slower
+// with the registers that this one wants).
+template <typename T, bool SCALED, int D, int NQ, bool JOIN>
 __global__ void __launch_bounds__(prompt_threads<NQ>(), NQ == 1 ? 2 : 1)
 window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, WindowParams p) {
@@ -127,14 +135,16 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     __shared__ PromptShared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cluster = JOIN ? p.cluster : 1;
+    const int rank = JOIN ? blockIdx.x % cluster : 0, unit = blockIdx.x / cluster;
     // later positions first: they see the most keys
-    const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv % p.B;
-    const int pair = p.row_tiles - 1 - (int)(blockIdx.x / p.Hkv / p.B);
+    const int h = unit % p.Hkv, b = unit / p.Hkv % p.B;
+    const int pair = p.row_tiles - 1 - unit / p.Hkv / p.B;
     const int seq = p.b0 + b;                         // E4M3: the workspace holds some sequences at a time
     const int per = kRows / p.G;                      // tokens of a row tile
-    const QuerySpan s = query_span(p, seq, h == 0 && pair == p.row_tiles - 1 && tid == 0);
+    const QuerySpan s = query_span(p, seq, h == 0 && rank == 0 && pair == p.row_tiles - 1 && tid == 0);
     const int t0 = pair * NQ * per;
-    if (t0 >= s.n) return;
+    if (t0 >= s.n) return;                            // the same for the whole cluster
     const int t_end = min(s.n, t0 + NQ * per);
     const Pages pages = visible_pages(s.first + t0, s.first + t_end - 1, p.window, p.sinks, p.P);
     const int ppt = kKeys / p.P;                      // pages of a key tile
@@ -148,7 +158,13 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const int last = s.first + min(s.n, t0 + (i + 1) * per) - 1;
         tiles[i] = t0 + i * per >= s.n || last < 0 ? 0 : (pages.head + max(last / p.P - pages.body0 + 1, 0) + ppt - 1) / ppt;
     }
-    const int n = max(tiles[0], tiles[1]);
+    // this CTA's stretch: key tiles j0 .. j0 + n of the list, numbered from 0 below
+    const int all = max(tiles[0], tiles[1]);
+    const int j0 = JOIN ? all * rank / cluster : 0, n = JOIN ? all * (rank + 1) / cluster - j0 : all;
+    if constexpr (JOIN) {
+        tiles[0] = min(max(tiles[0] - j0, 0), n);
+        tiles[1] = min(max(tiles[1] - j0, 0), n);
+    }
 
     if (tid == 0) {
         mbar_init(&sh.q_full, 1);
@@ -193,6 +209,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
 
+    float m = -INFINITY, l = 0.f;                     // of a softmax thread's row
     if (warp < MMA) {
         // ------------------------------------------------------------ softmax
         const int i = warp >> 2;
@@ -203,7 +220,8 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const int first = s.first + t0 + i * per, last = s.first + min(s.n, t0 + (i + 1) * per) - 1;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor memory lane of this warp, bits 16 up
         const uint32_t sa = tmem + lanes + S_COL[i], oa = tmem + lanes + O_COL[i];
-        float m = live ? -INFINITY : 0.f, l = 0.f, vscale = 1.f;
+        float vscale = 1.f;
+        if (!live) m = 0.f;
         bool ok = true;
         // Key tiles [whole0, whole1) are seen as a whole by every row of the row tile:
         // full tiles of window pages up to the first row's position (tiles of sinks
@@ -214,6 +232,8 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             whole0 = (pages.head + max(clear - pages.body0, 0) + ppt - 1) / ppt;
             if (pages.head > 0) whole0 = max(whole0, (pages.head + ppt - 1) / ppt);
             whole1 = (pages.head + max((first + 1) / p.P - pages.body0, 0)) / ppt;
+            whole0 -= j0;
+            whole1 -= j0;
         }
         bool unset = true;                    // a row of the warp has seen nothing yet
         if constexpr (SCALED) {
@@ -234,7 +254,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 if (masked) {
 #pragma unroll
                     for (int q = 0; q < kKeys / 16; ++q) {
-                        const int k = j * ppt + q * 16 / p.P, pg = pages.page(k);
+                        const int k = (j0 + j) * ppt + q * 16 / p.P, pg = pages.page(k);
                         const int base = pg * p.P + q * 16 % p.P;
                         uint32_t seen = 0;
                         if (k < pages.count && (!bad || good_page(p, table, pg)))
@@ -313,7 +333,9 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             ok = wait(&sh.pv_done[i], (tiles[i] - 1) & 1);
             tc_fence_after();
         }
-        if (ok) {
+        if constexpr (JOIN) {
+            if (!ok) { m = -INFINITY; l = 0.f; }      // reported; the others' shares are joined all the same
+        } else if (ok) {
             float inv = l > 0.f ? 1.f / l : 0.f;      // a row that sees nothing is zero
             if constexpr (SCALED) inv *= tiles[i] > 0 ? fp8_scale(sh.vmax) : 0.f;
             T *dst = static_cast<T *>(p.out) + (((size_t)seq * p.T + tok) * p.Hq + h * p.G + g) * D;
@@ -420,7 +442,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         if constexpr (SCALED) call = visible_pages(s.first, s.first + s.n - 1, p.window, p.sinks, p.P);
         float2 amax = make_float2(0.f, 0.f);                    // of the lane's page
         auto look_up = [&](int j) {                             // its first pool row, or -1
-            const int k = j * ppt + lane / NB;
+            const int k = (j0 + j) * ppt + lane / NB;
             if (lane >= ppt * NB || j >= n || k >= pages.count) return -1;
             const int pg = pages.page(k), phys = table[pg];
             if (phys >= 0 && phys < p.num_phys) {
@@ -490,7 +512,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             ok = wait(&sh.kv_full[st], vi / NS & 1);
             if (!ok) break;
             const bool bad = *(volatile int *)&sh.any_bad != 0;
-            const int k0 = j * ppt, k1 = k0 + ppt;
+            const int k0 = (j0 + j) * ppt, k1 = k0 + ppt;
             if ((bad || k1 >= pages.count || (pages.lo > 0 && k0 <= pages.head && k1 >= pages.head))) {
                 for (int r = lane; r < kKeys; r += 32) {
                     const int k = k0 + r / p.P, pg = pages.page(k), at = pg * p.P + r % p.P;
@@ -523,6 +545,68 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         if (n > 0) (void)mbar_wait_bounded(&sh.q_full, 0, p.drain_limit_ns);
         for (int st = 0; st < NS; ++st)
             if (sh.armed[st] > 0) (void)mbar_wait_bounded(&sh.kv_full[st], (sh.armed[st] - 1) & 1, p.drain_limit_ns);
+    }
+    if constexpr (JOIN) {
+        // Rows of D + 4 floats over the queries and the ring, which nothing uses any
+        // more; the cluster's CTAs join and write a share of the rows each.
+        constexpr int PITCH = D + 4;
+        float *part = reinterpret_cast<float *>(qtile);
+        float2 *state = reinterpret_cast<float2 *>(part + NQ * kRows * PITCH);    // maximum and sum of every row
+        static_assert(NQ * kRows * (PITCH * 4 + 8) <= NQ * NB * BLOCK + NS * kv_bytes<D>(), "partial outputs");
+        __syncthreads();                              // the copies' end, had one of the waits given up
+        tc_fence_after();
+        if (warp < MMA) {
+            const int i = warp >> 2, row = tid & 127;
+            const uint32_t oa = tmem + ((uint32_t)(warp & 3) << 21) + NQ * 128 + i * D;
+            state[i * kRows + row] = make_float2(m, tiles[i] > 0 ? l : 0.f);
+            if (tiles[i] > 0)
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(oa + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4 *>(part + (i * kRows + row) * PITCH + c + e) =
+                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+        }
+        tc_fence_before();
+        cluster_sync();
+        if (warp < MMA) {
+            const float unitv = SCALED ? fp8_scale(sh.vmax) : 1.f;
+            const int rows0 = min(per, s.n - t0) * p.G, rows1 = NQ == 2 ? min(per, max(s.n - t0 - per, 0)) * p.G : 0;
+            for (int x = rank * MMA * 32 + tid; x < (rows0 + rows1) * (D / 4); x += cluster * MMA * 32) {
+                const int y = x / (D / 4), c = x % (D / 4) * 4, i = y >= rows0, row = i ? y - rows0 : y, r = i * kRows + row;
+                float2 ml[kMostJoined];
+                float4 v[kMostJoined];
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < kMostJoined; ++k)
+                    if (k < cluster) {
+                        ml[k] = ld_cluster_v2(map_rank(state + r, k));
+                        v[k] = ld_cluster_v4(map_rank(part + r * PITCH + c, k));   // anything where the sum is 0
+                    }
+#pragma unroll
+                for (int k = 0; k < kMostJoined; ++k)
+                    if (k < cluster && ml[k].y > 0.f) top = fmaxf(top, ml[k].x);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kMostJoined; ++k)
+                    if (k < cluster && ml[k].y > 0.f) {
+                        const float f = exp2_fast(ml[k].x - top);
+                        sum = fmaf(f, ml[k].y, sum);
+                        o.x = fmaf(f, v[k].x, o.x); o.y = fmaf(f, v[k].y, o.y);
+                        o.z = fmaf(f, v[k].z, o.z); o.w = fmaf(f, v[k].w, o.w);
+                    }
+                const float inv = sum > 0.f ? unitv / sum : 0.f;   // a row that sees nothing is zero
+                const int tok = t0 + i * per + row / p.G;
+                T *dst = static_cast<T *>(p.out) + (((size_t)seq * p.T + tok) * p.Hq + h * p.G + row % p.G) * D + c;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(mma16816<T>::pack2(o.x * inv, o.y * inv),
+                                                             mma16816<T>::pack2(o.z * inv, o.w * inv));
+            }
+        }
+        cluster_sync();                               // nobody leaves while its part is read
     }
     if (warp == MMA) {
         tc_fence_after();
@@ -564,16 +648,36 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(WindowParams p, int d
 template <typename T, bool SCALED, int D>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, WindowParams p, cudaStream_t stream) {
     constexpr int NQ = D == 64 ? 1 : 2;
-    auto kernel = window_prompt_kernel<T, SCALED, D, NQ>;
     constexpr size_t smem = prompt_smem<D, NQ>();
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     const int per = NQ * (kRows / p.G);
     p.row_tiles = (p.T + per - 1) / per;
-    const long long blocks = (long long)p.row_tiles * p.B * p.Hkv;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kernel<<<(unsigned)blocks, prompt_threads<NQ>(), smem, stream>>>(q, k, v, p);
-    return cudaGetLastError();
+    const long long units = (long long)p.row_tiles * p.B * p.Hkv;
+    // As many CTAs to a unit as fill the SMs, while each has two key tiles.  Clusters of
+    // more than four find no place together in every part of the device: past half of
+    // the slots they run one after another (4 x 16 tokens over 8192, window 2048, d 128:
+    // 30.8 us with eight, 20.6 us with four).
+    const long long slots = (NQ == 1 ? 2 : 1) * (long long)p.sms;
+    const long long fill = slots / units, work = p.most_tiles / (2 * kKeys / 16);
+    p.cluster = (int)(fill < work ? fill : work);
+    if (p.cluster < 1) p.cluster = 1;
+    if (p.cluster > kMostJoined) p.cluster = kMostJoined;
+    if (p.cluster > 4 && units * p.cluster > slots / 2) p.cluster = 4;
+    if (units * p.cluster > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    auto kernel = p.cluster > 1 ? window_prompt_kernel<T, SCALED, D, NQ, true> : window_prompt_kernel<T, SCALED, D, NQ, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * p.cluster));
+    cfg.blockDim = dim3(prompt_threads<NQ>());
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = p.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, q, k, v, p);
 }
 
 }  // namespace

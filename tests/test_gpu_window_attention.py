@@ -327,3 +327,16 @@ def test_two_calls_at_once_on_two_streams(dtype):
     torch.cuda.synchronize()
     for a, b in zip(alone, outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("hkv,group,d,T,L", [(1, 8, 128, 20, 2500), (2, 4, 64, 40, 1300), (1, 1, 64, 300, 900), (4, 8, 128, 17, 700),
+                                             (1, 6, 128, 43, 4000)])
+def test_few_prompt_rows_over_many_keys(dtype, hkv, group, d, T, L):
+    # clusters that share the key tiles, of every size that these lengths give, some CTAs without any
+    lens, n = [L, 150 + T, T], [T, T, 3]
+    c = R.Paged(dtype, lens, hkv, d, 32, seed=27, amax_spread=1.0)
+    q = _queries(c, T, hkv * group, seed=5, scale=1.5)
+    for window, sinks in ((None, 0), (400, 70)):
+        out = _run(c, q, n, window, sinks, T)
+        _check(c, q, out, n, window, sinks)
