@@ -250,8 +250,8 @@ def kv_append(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Te
 # The stream and device lookups below are the ones behind torch.cuda.current_stream()
 # and torch.cuda.current_device(), without the Stream object and the initialisation
 # check: a decode step's append takes less time than those do.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_get_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # a torch without CUDA has neither
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, index: int):

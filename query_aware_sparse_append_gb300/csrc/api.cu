@@ -439,12 +439,13 @@ long long most_visible_tiles(int max_pages, int P, int T, int window, int sinks)
     return seen < all ? seen : all;
 }
 
-// CTAs per unit of the few-rows kernel: what fills the SMs with four CTAs each, so
-// that all run at once, as long as every warp has a tile: with few units
-// the chain of a warp's tiles is what a call takes.
-int window_cluster(long long units, long long tiles) {
+// CTAs per unit of the few-rows kernel: what fills the SMs with as many CTAs as their
+// registers hold, so that all run at once, as long as every warp has a tile: with few
+// units the chain of a warp's tiles is what a call takes.
+int window_cluster(qasa_dtype dt, int rows, long long units, long long tiles) {
     const int sms = sm_count() > 0 ? sm_count() : 152;
-    const long long fill = 4LL * sms / (units > 0 ? units : 1), work = tiles / 4;
+    const int per_sm = dt == QASA_DTYPE_F32 ? (rows == 1 ? 4 : 2) : rows <= 8 ? 4 : 3;
+    const long long fill = (long long)per_sm * sms / (units > 0 ? units : 1), work = tiles / 4;
     const long long c = fill < work ? fill : work;
     return c < 1 ? 1 : c > 8 ? 8 : (int)c;
 }
@@ -583,6 +584,12 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     if (st != QASA_OK) return st;
     if ((reinterpret_cast<uintptr_t>(q_lens) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
         return QASA_ERR_ALIGN;
+    // one sequence's unpacked pages have to be within a tensor map's 32-bit rows
+    const bool unpacks = cache->dtype == QASA_DTYPE_E4M3 &&
+                         !window_few_rows(cache->dtype, (long long)max_q_tokens * (num_q_heads / cache->num_kv_heads));
+    if (unpacks && (long long)window_unpacked(cache, 1, max_q_tokens, max_pages_per_seq, window, sink_tokens).pages *
+                           cache->num_kv_heads * cache->page_size > 0x7fffffffLL)
+        return QASA_ERR_SHAPE;
     const size_t need = qasa_window_workspace_size(batch, num_q_heads, cache, max_q_tokens, max_pages_per_seq, window,
                                                    sink_tokens);
     if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return QASA_ERR_WORKSPACE;
@@ -645,7 +652,7 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
         return QASA_OK;
     }
     const long long units = (long long)batch * p.Hkv * window_row_tiles(cache->dtype, p.T * p.G);
-    p.cluster = window_cluster(units, most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens));
+    p.cluster = window_cluster(cache->dtype, p.T * p.G, units, most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens));
     if (units * p.cluster > 0x7fffffffLL) return QASA_ERR_SHAPE;
     const cudaError_t e = launch_window_rows(cache->dtype, cache->head_dim, p, stream);
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;

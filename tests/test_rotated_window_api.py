@@ -115,3 +115,26 @@ def test_rotation_table_keeps_far_angles(lib):
     import math
     assert abs(float(t[99_999, 0, 3]) - math.cos(angle)) <= 2.0 ** -24
     assert abs(float(t[99_999, 1, 3]) - math.sin(angle)) <= 2.0 ** -24
+
+
+def test_unpacked_e4m3_pages_beyond_32_bit_rows_are_refused(lib):
+    # 16384 visible pages x 16 slots x 8192 heads are 2^31 rows of the workspace; few rows need none
+    many = _cache(lib, dtype=3, page_scales=0x90000, num_phys_pages=1, num_kv_heads=8192)
+    kw = dict(hq=8192, maxp=16384, window=1 << 30, batch=1, ws=0xA0000, wsb=1 << 40)
+    assert _attend(lib, cache=many, T=200, **kw) == 3
+    assert lib._lib.qasa_window_workspace_size(1, 8192, ctypes.byref(many), 128, 16384, 1 << 30, 0) == 0
+
+
+def test_workspace_sizes(lib):
+    f = lib._lib.qasa_window_workspace_size
+    e4m3, f16 = _cache(lib, dtype=3, page_scales=0x90000), _cache(lib)
+    assert f(2, 32, ctypes.byref(f16), 4096, 512, 1024, 16) == 0
+    assert f(2, 32, ctypes.byref(e4m3), 16, 512, 1024, 16) == 0           # 128 rows: read as they are
+    # 17 tokens of 8 heads: the pages of 1024 + 16 tokens, not aligned, and one of sinks
+    pages = (1024 + 17 + 14) // 16 + 1 + 1
+    assert f(2, 32, ctypes.byref(e4m3), 17, 512, 1024, 16) == 2 * pages * 4 * 16 * 128 * 4
+    assert f(2, 32, ctypes.byref(e4m3), 17, 20, 1024, 16) == 2 * 20 * 4 * 16 * 128 * 4
+    for bad in ((0, 32, 17, 512, 1024, 16), (2, 3, 17, 512, 1024, 16), (2, 32, 0, 512, 1024, 16), (2, 32, 17, 0, 1024, 16),
+                (2, 32, 17, 512, 0, 16), (2, 32, 17, 512, 1024, -1)):
+        assert f(bad[0], bad[1], ctypes.byref(e4m3), *bad[2:]) == 0
+    assert f(2, 32, None, 17, 512, 1024, 16) == 0
