@@ -336,7 +336,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         if constexpr (JOIN) {
             if (!ok) { m = -INFINITY; l = 0.f; }      // reported; the others' shares are joined all the same
         } else if (ok) {
-            float inv = l > 0.f ? 1.f / l : 0.f;      // a row that sees nothing is zero
+            float inv = l != 0.f ? 1.f / l : 0.f;     // a row that sees nothing is zero; a NaN query's sum is NaN
             if constexpr (SCALED) inv *= tiles[i] > 0 ? fp8_scale(sh.vmax) : 0.f;
             T *dst = static_cast<T *>(p.out) + (((size_t)seq * p.T + tok) * p.Hq + h * p.G + g) * D;
 #pragma unroll
@@ -349,7 +349,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0;
                 }
-                if (live && l > 0.f) {
+                if (live && l != 0.f) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         float v[8];
@@ -589,17 +589,17 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     }
 #pragma unroll
                 for (int k = 0; k < kMostJoined; ++k)
-                    if (k < cluster && ml[k].y > 0.f) top = fmaxf(top, ml[k].x);
+                    if (k < cluster && ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < kMostJoined; ++k)
-                    if (k < cluster && ml[k].y > 0.f) {
+                    if (k < cluster && ml[k].y != 0.f) {          // NaN included: it goes through to the row
                         const float f = exp2_fast(ml[k].x - top);
                         sum = fmaf(f, ml[k].y, sum);
                         o.x = fmaf(f, v[k].x, o.x); o.y = fmaf(f, v[k].y, o.y);
                         o.z = fmaf(f, v[k].z, o.z); o.w = fmaf(f, v[k].w, o.w);
                     }
-                const float inv = sum > 0.f ? unitv / sum : 0.f;   // a row that sees nothing is zero
+                const float inv = sum != 0.f ? unitv / sum : 0.f;  // a row that sees nothing is zero
                 const int tok = t0 + i * per + row / p.G;
                 T *dst = static_cast<T *>(p.out) + (((size_t)seq * p.T + tok) * p.Hq + h * p.G + row % p.G) * D + c;
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(mma16816<T>::pack2(o.x * inv, o.y * inv),

@@ -38,7 +38,8 @@ constexpr int kMaxCluster = 8;
 
 // Joins the partial states of a unit and writes its rows.  Every warp of the CTA
 // has left ROWS rows of o[D] and (m, l) in shared memory: m the running maximum
-// in log2 units (-inf where the warp saw nothing), l the sum of weights.
+// in log2 units (-inf where the warp saw nothing), l the sum of weights: 0 where it
+// saw nothing, NaN of a query that has one, whose scores no maximum takes up.
 template <typename T, int D, int ROWS, int W>
 __device__ __forceinline__ void join_and_write(const WindowParams &p, float *part_o, float2 *part_ml, int cluster,
                                                int row0, int rows, int b, int h) {
@@ -55,7 +56,7 @@ __device__ __forceinline__ void join_and_write(const WindowParams &p, float *par
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const float2 ml = part_ml[w * ROWS + r];
-            if (ml.x == -INFINITY) continue;
+            if (ml.y == 0.f) continue;
             const float f = exp2f(ml.x - m);
             const float4 v = reinterpret_cast<const float4 *>(part_o + ((size_t)w * ROWS + r) * D)[c];
             l = fmaf(f, ml.y, l);
@@ -84,7 +85,7 @@ __device__ __forceinline__ void join_and_write(const WindowParams &p, float *par
                 }
 #pragma unroll
             for (int k = 0; k < kMaxCluster; ++k)
-                if (k < cluster && ml[k].x != -INFINITY) {
+                if (k < cluster && ml[k].y != 0.f) {
                     const float4 v = ld_cluster_v4(map_rank(part_o + (size_t)r * D + 4 * c, k));
                     const float f = exp2f(ml[k].x - m);
                     l = fmaf(f, ml[k].y, l);
@@ -92,7 +93,7 @@ __device__ __forceinline__ void join_and_write(const WindowParams &p, float *par
                     o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
                 }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that sees nothing is zero
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero
         const int row = row0 + r, t = row / p.G, g = row % p.G;
         T *dst = static_cast<T *>(p.out) + (((size_t)b * p.T + t) * p.Hq + h * p.G + g) * D + 4 * c;
         if constexpr (sizeof(T) == 4) {
