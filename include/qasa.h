@@ -318,7 +318,10 @@ qasa_status qasa_dense_decode_attention(const qasa_kv_cache *cache, const void *
  *                  aligned (scratch, no initialisation; NULL where that is 0: it is
  *                  only prompts over an E4M3 cache, more than 128 query rows per KV
  *                  head, that need any, for the visible pages as halves; at most
- *                  512 MiB, or one sequence's)
+ *                  512 MiB, or one sequence's).  A smaller one serves too, down to the
+ *                  size for a batch of one, with fewer sequences at a time: so memory
+ *                  of the size for a larger batch, max_q_tokens, max_pages_per_seq,
+ *                  window and sink_tokens serves every call within them
  * Any group size 1..8, max_q_tokens up to 65536.  Pages that hold no token that
  * some query of the sequence sees are not read, and neither are their block-table
  * entries: a rolling cache may have given them back.  Keys and values of tokens

@@ -363,7 +363,7 @@ def _tokens(n: Optional[int]) -> int:
 
 def alloc_window_workspace(cache: PagedKVCache, batch: int, num_q_heads: int, max_q_tokens: int,
                            max_pages_per_seq: int, window: Optional[int] = None, sink_tokens: int = 0) -> torch.Tensor:
-    """Workspace of window_attention calls of up to this shape with this window."""
+    """Workspace of window_attention calls of up to this batch, these tokens, pages, window and sinks."""
     n = int(_lib.qasa_window_workspace_size(batch, num_q_heads, cache.c_ref, max_q_tokens, max_pages_per_seq,
                                             _tokens(window), _tokens(sink_tokens)))
     return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_pool.device)

@@ -395,11 +395,14 @@ bool window_few_rows(qasa_dtype dt, long long rows) {
 }
 
 // Workspace of the prompt kernel for an E4M3 cache: the visible pages of `group`
-// sequences as halves, keys then values.  As many sequences as fit half a GiB go at
-// once, at least one.
+// sequences as halves, keys then values.  As many sequences as fit half a GiB and the
+// workspace that is given go at once.  `one`, a sequence's share and the least that a
+// call needs, grows with tokens, pages, window and sinks, so a workspace made for a
+// larger call always holds it; the size for a whole group does not grow with them (a
+// smaller share may let one more sequence in).
 struct Unpacked {
     int pages, group;
-    size_t bytes;
+    size_t one;
 };
 
 Unpacked window_unpacked(const qasa_kv_cache *c, int batch, int T, int max_pages, int window, int sinks) {
@@ -412,7 +415,7 @@ Unpacked window_unpacked(const qasa_kv_cache *c, int batch, int T, int max_pages
     long long g = (512LL << 20) / one;
     if (g > rows) g = rows;
     u.group = (int)(g < 1 ? 1 : g > batch ? batch : g);
-    u.bytes = (size_t)(one * u.group);
+    u.one = (size_t)one;
     return u;
 }
 
@@ -566,7 +569,8 @@ size_t qasa_window_workspace_size(int32_t batch, int32_t num_q_heads, const qasa
         cache->page_size < 1 || cache->head_dim < 1)
         return 0;
     if (window_few_rows(cache->dtype, (long long)max_q_tokens * (num_q_heads / cache->num_kv_heads))) return 0;
-    return window_unpacked(cache, batch, max_q_tokens, max_pages_per_seq, window, sink_tokens).bytes;
+    const Unpacked u = window_unpacked(cache, batch, max_q_tokens, max_pages_per_seq, window, sink_tokens);
+    return u.one * u.group;
 }
 
 qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
@@ -584,15 +588,15 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     if (st != QASA_OK) return st;
     if ((reinterpret_cast<uintptr_t>(q_lens) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
         return QASA_ERR_ALIGN;
-    // one sequence's unpacked pages have to be within a tensor map's 32-bit rows
-    const bool unpacks = cache->dtype == QASA_DTYPE_E4M3 &&
-                         !window_few_rows(cache->dtype, (long long)max_q_tokens * (num_q_heads / cache->num_kv_heads));
-    if (unpacks && (long long)window_unpacked(cache, 1, max_q_tokens, max_pages_per_seq, window, sink_tokens).pages *
-                           cache->num_kv_heads * cache->page_size > 0x7fffffffLL)
-        return QASA_ERR_SHAPE;
-    const size_t need = qasa_window_workspace_size(batch, num_q_heads, cache, max_q_tokens, max_pages_per_seq, window,
-                                                   sink_tokens);
-    if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return QASA_ERR_WORKSPACE;
+    const bool few = window_few_rows(cache->dtype, (long long)max_q_tokens * (num_q_heads / cache->num_kv_heads));
+    Unpacked u{0, batch, 0};
+    if (cache->dtype == QASA_DTYPE_E4M3 && !few) {
+        u = window_unpacked(cache, batch, max_q_tokens, max_pages_per_seq, window, sink_tokens);
+        // one sequence's unpacked pages have to be within a tensor map's 32-bit rows
+        if ((long long)u.pages * cache->num_kv_heads * cache->page_size > 0x7fffffffLL) return QASA_ERR_SHAPE;
+        if (!workspace || workspace_bytes < u.one || !aligned16(workspace)) return QASA_ERR_WORKSPACE;
+        if (workspace_bytes / u.one < (size_t)u.group) u.group = (int)(workspace_bytes / u.one);
+    }
     WindowParams p;
     p.q = q;
     p.out = out;
@@ -624,26 +628,23 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     p.ws_pages = 0;
     p.sms = sm_count() > 0 ? sm_count() : 1;
     p.most_tiles = most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens);
-    if (!window_few_rows(cache->dtype, (long long)p.T * p.G)) {
+    if (!few) {
         CUtensorMap qm, km, vm;
         st = query_tensor_map(&qm, q, cache->dtype, cache->head_dim, num_q_heads, p.G, (long long)batch * p.T);
         if (st != QASA_OK) return st;
         qasa_kv_cache pages = *cache;             // what the tensor maps show
-        int group = batch;
         if (cache->dtype == QASA_DTYPE_E4M3) {
-            const Unpacked u = window_unpacked(cache, batch, p.T, max_pages_per_seq, window, sink_tokens);
-            group = u.group;
             p.ws_pages = u.pages;
             pages.dtype = QASA_DTYPE_F16;
             pages.num_phys_pages = u.group * u.pages;
             pages.k_pool = workspace;
-            pages.v_pool = static_cast<unsigned char *>(workspace) + u.bytes / 2;
+            pages.v_pool = static_cast<unsigned char *>(workspace) + u.one / 2 * u.group;
         }
         st = pool_tensor_map(&km, pages.k_pool, &pages, false);
         if (st == QASA_OK) st = pool_tensor_map(&vm, pages.v_pool, &pages, false);
         if (st != QASA_OK) return st;
-        for (p.b0 = 0; p.b0 < batch; p.b0 += group) {
-            p.B = batch - p.b0 < group ? batch - p.b0 : group;
+        for (p.b0 = 0; p.b0 < batch; p.b0 += u.group) {
+            p.B = batch - p.b0 < u.group ? batch - p.b0 : u.group;
             cudaError_t pe = cudaSuccess;
             if (p.ws_pages) pe = launch_unpack_codes(cache->head_dim, p, pages.k_pool, pages.v_pool, stream);
             if (pe == cudaSuccess) pe = launch_window_prompt(cache->dtype, cache->head_dim, qm, km, vm, p, stream);
