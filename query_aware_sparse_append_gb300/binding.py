@@ -7,6 +7,7 @@ Importing this module loads ``libqasa.so``; a missing library raises at once
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -290,6 +291,13 @@ def _call_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
     return stream.cuda_stream
 
 
+def _allocating_on(stream: Optional[torch.cuda.Stream]):
+    """Context whose tensors belong to the stream of a call: memory that the current stream gave back, and may
+    still be working on, is not handed to a kernel on `stream`, nor theirs to the current stream while `stream`
+    works on it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def rotation_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """Cosines and sines of the angles pos * base^(-2 i / rot_dim), [max_positions, 2, rot_dim / 2]
     float32, computed in 64 bits (a far position's angle has few 32-bit digits left).  Any other
@@ -306,7 +314,7 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
                       stream=None) -> Optional[torch.Tensor]:
     """kv_append with the position rotation applied on the way: k_new [B, T, Hkv, d] is rotated by the
     table's angles of its positions before it is stored, q [B, T, Hq, d] (optional) is rotated into
-    q_out [B, T, Hq, d] (contiguous, allocated where not given, returned).  k_new, v_new and q may be
+    q_out [B, T, Hq, d] (contiguous, allocated on the call's stream where not given, returned).  k_new, v_new and q may be
     parts of one tensor: any batch and token stride that is a multiple of 16 bytes.  table: as made by
     rotation_table, whose last dimension says how many channels turn; interleaved: neighbouring
     channels are the pairs (else channels rot_dim / 2 apart)."""
@@ -336,7 +344,8 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
         if qb != B or qt != T or qd != d:
             raise ValueError("q must have the batch and tokens of k_new and the cache's head_dim")
         if q_out is None:
-            q_out = torch.empty((B, T, hq, d), dtype=value, device=q.device)
+            with _allocating_on(stream):
+                q_out = torch.empty((B, T, hq, d), dtype=value, device=q.device)
         out = _arg(q_out, "q_out", value, (B, T, hq, d), index)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -377,7 +386,8 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
     """Attention of the newest tokens of every sequence: q [B, T, Hq, d] (or [B, Hq, d], one token each)
     holds the queries of the last q_lens[b] (default T) of its seq_lens[b] tokens, each of which sees
     itself and what came before within `window` tokens (None: everything) and the first `sink_tokens`.
-    Rows at or past q_lens[b] of `out` are left as they were (unset where it is allocated here)."""
+    Rows at or past q_lens[b] of `out` are left as they were (unset where it is allocated here, on the call's
+    stream)."""
     index = cache.device_index
     if index >= 0 and _get_device() != index:
         with torch.cuda.device(index):
@@ -396,13 +406,13 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
         raise ValueError("block_table must be [batch, max_pages_per_seq]")
     maxp = block_table.shape[1]
     qp = _arg(q, "q", value, shape, index)
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = alloc_window_workspace(cache, B, hq, T, maxp, window, sink_tokens)
-        if stream is not None:
-            workspace.record_stream(stream)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
+    if out is None or workspace is None:
+        with _allocating_on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = alloc_window_workspace(cache, B, hq, T, maxp, window, sink_tokens)
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous memory on cuda:%d" % index)
     if index < 0:
         raise ValueError("the cache must be on a CUDA device")
