@@ -163,6 +163,13 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _allocating_on(stream: Optional[torch.cuda.Stream]):
+    """Context whose tensors belong to the stream of a call: memory that the current stream gave back, and may
+    still be working on, is not handed to a kernel on `stream`, nor theirs to the current stream while `stream`
+    works on it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _contig(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -289,13 +296,6 @@ def _call_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
     if stream.device_index != index:
         raise ValueError("stream and cache are on different devices")
     return stream.cuda_stream
-
-
-def _allocating_on(stream: Optional[torch.cuda.Stream]):
-    """Context whose tensors belong to the stream of a call: memory that the current stream gave back, and may
-    still be working on, is not handed to a kernel on `stream`, nor theirs to the current stream while `stream`
-    works on it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def rotation_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -461,12 +461,13 @@ def select_pages(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Tensor
                  workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
     B, Hq = int(q.shape[0]), int(q.shape[1])
-    bud = budget_pages(budget, seq_lens, cache.page_size)
-    if selected is None:
-        selected = torch.empty((B, cache.num_kv_heads, max_budget), dtype=torch.int32,
-                               device=q.device)
-    if workspace is None:
-        workspace = alloc_workspace(cache, B, Hq, int(block_table.shape[1]))
+    with _allocating_on(stream):
+        bud = budget_pages(budget, seq_lens, cache.page_size)
+        if selected is None:
+            selected = torch.empty((B, cache.num_kv_heads, max_budget), dtype=torch.int32,
+                                   device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(cache, B, Hq, int(block_table.shape[1]))
     code = _lib.qasa_select_pages(cache.c_ref, _ptr(_contig(q, "q")), Hq, _ptr(block_table),
                                   int(block_table.shape[1]), _ptr(seq_lens), _ptr(bud), max_budget,
                                   _ptr(selected), _ptr(scores), _ptr(workspace),
@@ -481,11 +482,12 @@ def sparse_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
                      workspace: Optional[torch.Tensor] = None,
                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     B, Hq = int(q.shape[0]), int(q.shape[1])
-    bud = budget_pages(budget, seq_lens, cache.page_size)
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = alloc_workspace(cache, B, Hq, int(block_table.shape[1]))
+    with _allocating_on(stream):
+        bud = budget_pages(budget, seq_lens, cache.page_size)
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_workspace(cache, B, Hq, int(block_table.shape[1]))
     code = _lib.qasa_sparse_attention(cache.c_ref, _ptr(_contig(q, "q")), Hq, _ptr(block_table),
                                       int(block_table.shape[1]), _ptr(seq_lens), _ptr(bud),
                                       int(selected.shape[-1]), _ptr(selected),
@@ -506,16 +508,17 @@ def sparse_decode_attention(cache: PagedKVCache, q: torch.Tensor, block_table: t
     """One decode step: (out [B, Hq, d], selected [B, Hkv, max_budget] ascending, -1 padded)."""
     B, Hq = int(q.shape[0]), int(q.shape[1])
     maxp = int(block_table.shape[1])
-    bud = budget_pages(budget, seq_lens, cache.page_size)
     if max_budget is None:
         max_budget = selected.shape[-1] if selected is not None else max(2, maxp)
-    if out is None:
-        out = torch.empty_like(q)
-    if selected is None:
-        selected = torch.empty((B, cache.num_kv_heads, max_budget), dtype=torch.int32,
-                               device=q.device)
-    if workspace is None:
-        workspace = alloc_workspace(cache, B, Hq, maxp)
+    with _allocating_on(stream):
+        bud = budget_pages(budget, seq_lens, cache.page_size)
+        if out is None:
+            out = torch.empty_like(q)
+        if selected is None:
+            selected = torch.empty((B, cache.num_kv_heads, max_budget), dtype=torch.int32,
+                                   device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(cache, B, Hq, maxp)
     code = _lib.qasa_sparse_decode_attention(cache.c_ref, _ptr(_contig(q, "q")), Hq,
                                              _ptr(block_table), maxp, _ptr(seq_lens), _ptr(bud),
                                              int(max_budget), float(scale or 0.0), _ptr(out),
@@ -536,7 +539,8 @@ def sparse_decode_attention_noalloc(cache: PagedKVCache, q: torch.Tensor, block_
     qasa.h).  The caller passes every input and output; returns the status code
     (QASA_ERR_WORKSPACE when the shape needs more scratch than the buffer)."""
     B, Hq = int(q.shape[0]), int(q.shape[1])
-    bud = budget if isinstance(budget, torch.Tensor) else budget_pages(budget, seq_lens, cache.page_size)
+    with _allocating_on(stream):
+        bud = budget if isinstance(budget, torch.Tensor) else budget_pages(budget, seq_lens, cache.page_size)
     return int(_lib.qasa_sparse_decode_attention_noalloc(
         cache.c_ref, _ptr(_contig(q, "q")), Hq, _ptr(block_table), int(block_table.shape[1]),
         _ptr(seq_lens), _ptr(bud), int(max_budget), float(scale or 0.0), _ptr(out), _ptr(selected),
@@ -563,7 +567,8 @@ def sparse_decode_attention_host(cache: PagedKVCache, q_host: torch.Tensor, bloc
     B, Hq = int(q_host.shape[0]), int(q_host.shape[1])
     maxp = int(block_table_host.shape[1])
     if workspace is None:
-        workspace = alloc_host_workspace(cache, B, Hq, maxp, max_budget)
+        with _allocating_on(stream):
+            workspace = alloc_host_workspace(cache, B, Hq, maxp, max_budget)
     code = _lib.qasa_sparse_decode_attention_host(
         cache.c_ref, _ptr(_contig(q_host, "q_host")), Hq, _ptr(_contig(block_table_host, "block_table_host")), maxp,
         _ptr(_contig(seq_lens_host, "seq_lens_host")), _ptr(_contig(budget_host, "budget_host")), int(max_budget),
@@ -588,10 +593,11 @@ def dense_decode_attention(cache: PagedKVCache, q: torch.Tensor, block_table: to
                            status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     B, Hq = int(q.shape[0]), int(q.shape[1])
     maxp = int(block_table.shape[1])
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = alloc_workspace(cache, B, Hq, maxp)
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_workspace(cache, B, Hq, maxp)
     code = _lib.qasa_dense_decode_attention(cache.c_ref, _ptr(_contig(q, "q")), Hq,
                                             _ptr(block_table), maxp, _ptr(seq_lens),
                                             float(scale or 0.0), _ptr(out), _ptr(workspace),
@@ -610,7 +616,8 @@ def page_attention_mass(cache: PagedKVCache, q: torch.Tensor, block_table: torch
     B, Hq = int(q.shape[0]), int(q.shape[1])
     maxp = int(block_table.shape[1])
     if mass is None:
-        mass = torch.zeros((B, cache.num_kv_heads, maxp), dtype=torch.float32, device=q.device)
+        with _allocating_on(stream):
+            mass = torch.zeros((B, cache.num_kv_heads, maxp), dtype=torch.float32, device=q.device)
     code = _lib.qasa_page_attention_mass(cache.c_ref, _ptr(_contig(q, "q")), Hq, _ptr(block_table), maxp,
                                          _ptr(seq_lens), float(scale or 0.0), _ptr(_contig(mass, "mass")),
                                          B, _ptr(status), _stream(stream))
@@ -626,9 +633,10 @@ def page_hit_rate(cache: PagedKVCache, mass: torch.Tensor, seq_lens: torch.Tenso
     the selection covers and the largest mass any k_b pages cover."""
     B, Hkv, maxp = (int(x) for x in mass.shape)
     mb = int(selected.shape[2])
-    hits = torch.empty((B, Hkv), dtype=torch.int32, device=mass.device)
-    covered = torch.empty((B, Hkv), dtype=torch.float32, device=mass.device)
-    best = torch.empty((B, Hkv), dtype=torch.float32, device=mass.device)
+    with _allocating_on(stream):
+        hits = torch.empty((B, Hkv), dtype=torch.int32, device=mass.device)
+        covered = torch.empty((B, Hkv), dtype=torch.float32, device=mass.device)
+        best = torch.empty((B, Hkv), dtype=torch.float32, device=mass.device)
     code = _lib.qasa_page_hit_rate(cache.c_ref, _ptr(_contig(mass, "mass")), maxp, _ptr(seq_lens),
                                    _ptr(budget_pages), mb, _ptr(_contig(selected, "selected")), B,
                                    _ptr(hits), _ptr(covered), _ptr(best), _ptr(status), _stream(stream))
