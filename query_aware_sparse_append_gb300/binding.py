@@ -163,11 +163,14 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _allocating_on(stream: Optional[torch.cuda.Stream]):
     """Context whose tensors belong to the stream of a call: memory that the current stream gave back, and may
     still be working on, is not handed to a kernel on `stream`, nor theirs to the current stream while `stream`
     works on it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _contig(t: torch.Tensor, name: str) -> torch.Tensor:
