@@ -328,7 +328,8 @@ qasa_status qasa_dense_decode_attention(const qasa_kv_cache *cache, const void *
  * that some query of the call sees must be finite; slots that none sees may hold
  * anything.  A query that holds a NaN gives a row of NaN where it sees a token, and
  * so does an infinite one unless all its scores are -infinity, which gives zeros;
- * no other row changes by more than its rounding.
+ * no other row changes by more than its rounding.  Where QASA_DEVERR_TIMEOUT is
+ * set, each row of out is right or as it was.
  */
 size_t qasa_window_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
                                   int32_t max_q_tokens, int32_t max_pages_per_seq, int32_t window,

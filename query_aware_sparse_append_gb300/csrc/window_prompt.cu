@@ -51,6 +51,7 @@ namespace {
 constexpr int kRows = 128;            // rows of a row tile
 constexpr int kKeys = 128;            // tokens of a key tile
 constexpr int kMostJoined = 8;        // CTAs that share the key tiles of their rows
+constexpr float kGivenUp = 3e38f;     // maximum that a CTA reports for rows that it gave up
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
@@ -63,7 +64,7 @@ struct PromptShared {
     uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], pv_done[2], vmax_ready, drained;
     uint32_t tmem;
     int any_bad;         // some page of this CTA has a bad block-table entry
-    int failed;          // a bounded wait gave up: nothing more is written
+    int failed;          // a bounded wait gave up: the rows that waited are not written
     int armed[kStages];  // copies into each stage so far
     float vmax;          // E4M3: the largest V amax among the CTA's pages
     float ks[kScaleRing][kKeys / 16], vamax[kScaleRing][kKeys / 16];
@@ -334,7 +335,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             tc_fence_after();
         }
         if constexpr (JOIN) {
-            if (!ok) { m = -INFINITY; l = 0.f; }      // reported; the others' shares are joined all the same
+            if (!ok) { m = kGivenUp; l = -1.f; }      // outweighs the other shares: the row's sum comes out negative
         } else if (ok) {
             float inv = l != 0.f ? 1.f / l : 0.f;     // a row that sees nothing is zero; a NaN query's sum is NaN
             if constexpr (SCALED) inv *= tiles[i] > 0 ? fp8_scale(sh.vmax) : 0.f;
@@ -599,6 +600,7 @@ window_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         o.x = fmaf(f, v[k].x, o.x); o.y = fmaf(f, v[k].y, o.y);
                         o.z = fmaf(f, v[k].z, o.z); o.w = fmaf(f, v[k].w, o.w);
                     }
+                if (sum < 0.f) continue;              // a CTA gave up: the row stays as it was
                 const float inv = sum != 0.f ? unitv / sum : 0.f;  // a row that sees nothing is zero
                 const int tok = t0 + i * per + row / p.G;
                 T *dst = static_cast<T *>(p.out) + (((size_t)seq * p.T + tok) * p.Hq + h * p.G + row % p.G) * D + c;

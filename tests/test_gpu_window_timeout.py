@@ -23,10 +23,11 @@ def _right(c, q, out, b, L, n):
 
 
 SINGLE = [400, 330]          # few keys: a CTA goes through all of its rows' keys itself
+SHARED = [1200, 900]        # clusters of four share a row's keys
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "e4m3"])
-@pytest.mark.parametrize("d,lens", [(128, SINGLE), (64, SINGLE)])
+@pytest.mark.parametrize("d,lens", [(128, SINGLE), (64, SINGLE), (128, SHARED), (64, SHARED)])
 def test_waits_that_run_out_are_reported_and_leave_rows_right_or_alone(dtype, d, lens, monkeypatch):
     from query_aware_sparse_append_gb300 import binding as qasa
     T = 300
