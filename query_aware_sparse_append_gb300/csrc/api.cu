@@ -556,6 +556,8 @@ qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotati
     p.rot = rotation->rot_dim;
     p.interleaved = rotation->interleaved;
     p.kv_blocks = 0;
+    p.q_span = 1;
+    p.sms = sm_count() > 0 ? sm_count() : 1;
     const cudaError_t e = launch_append_rotated(cache->dtype, cache->head_dim, p, batch, stream);
     if (e == cudaErrorInvalidConfiguration) return QASA_ERR_SHAPE;
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;

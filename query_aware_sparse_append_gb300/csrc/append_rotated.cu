@@ -498,11 +498,15 @@ cudaError_t launch_t(RotatedParams p, int batch, cudaStream_t stream) {
     constexpr int RPP = 32 / (D / (2 * chunk16<T>::n));
     const long long pages = ((long long)p.T + p.P - 2) / p.P + 1;   // the most that T tokens touch
     const long long kv = pages * ((2 * p.Hkv + kWarps - 1) / kWarps);
-    // A warp of the Q role takes one batch of heads while that leaves warps idle, and
-    // up to a whole token where there are enough tokens (2 x 4096 of 32 heads: 8 rows
-    // of a lane group per warp).
+    // A warp of the Q role takes one batch of heads.  Counts may leave tokens out, whose
+    // warps only come and go: from 12 warps to a quarter of an SM on (which holds five at
+    // a time) it then takes more, up to a whole token.  E4M3, counts between 1 and T,
+    // with a batch each and with a token: 16 x 1024 tokens of 32 heads 37.0 and 33.7 us,
+    // 8 x 1024 20.7 and 19.1, 16 x 512 of 64 heads 45.0 and 41.1 (a limit of 24 misses
+    // the second, one of 6 is level).  Without counts a token to a warp gives nothing:
+    // 2 x 4096 bf16 tokens 34.9 and 35.3 us, 1 x 1024 of 64 heads 8.8 and 9.5.
     const long long batches = (p.Hq + RPP * kBatch - 1) / (RPP * kBatch);
-    const long long spread = batches * p.T * batch / (24LL * 152 * 4);
+    const long long spread = p.append_lens ? batches * p.T * batch / (12LL * 4 * p.sms) : 1;
     p.q_span = (int)(spread < 1 ? 1 : spread < batches ? spread : batches > 0 ? batches : 1);
     const long long q = p.q ? ((batches + p.q_span - 1) / p.q_span * p.T + kWarps - 1) / kWarps : 0;
     if (kv + q > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -42,6 +42,7 @@ struct RotatedParams {
     int num_phys, Hkv, Hq, P, max_pages, T, max_positions, rot, interleaved;
     int kv_blocks;       // blocks in x of the KV role, the rest rotate q
     int q_span;          // batches of query heads that a warp rotates
+    int sms;             // SMs of the device
 };
 
 struct WindowParams {
