@@ -81,3 +81,22 @@ def test_the_others_are_as_in_a_call_of_their_own(dtype, break_, bits):
     if break_ is not _bad_page:
         assert bool((mine.k_pool[pages].view(torch.uint8) == fresh.k_pool[pages].view(torch.uint8)).all())
         assert bool((mine.v_pool[pages].view(torch.uint8) == fresh.v_pool[pages].view(torch.uint8)).all())
+
+
+def test_the_largest_number_of_tokens():
+    # rows of one token repeated (a stride of 0): the call has room for 2^31 - 1 tokens and appends 40
+    from query_aware_sparse_append_gb300 import binding as qasa
+    most = 2 ** 31 - 1
+    c = R.Paged("f16", [5], 1, D, PAGE, seed=93, reserve=40)
+    e = R.Paged("f16", [5], 1, D, PAGE, seed=93, reserve=40)
+    row = torch.randn((1, 1, 1, D), generator=torch.Generator(device="cpu").manual_seed(94)).half().cuda()
+    table = qasa.rotation_table(64, D)
+    n = torch.tensor([40], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for x, tokens in ((c, most), (e, 40)):
+        rows = row.expand(1, tokens, 1, D)
+        qasa.kv_append_rotated(x.library(), x.table, x.seq_lens, rows, rows, table, append_lens=n, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    for name in ("k_pool", "v_pool", "bounds"):
+        assert bool((getattr(c, name).view(torch.uint8) == getattr(e, name).view(torch.uint8)).all()), name
