@@ -387,9 +387,22 @@ qasa_status run_attention(const qasa_kv_cache *cache, const void *q, int num_q_h
 }
 
 // Whether the few-rows kernel serves a call with this many rows (tokens x heads of a
-// group).  16-bit: what one of its row tiles holds; the prompt kernel takes a row tile
-// of 128 in the time it takes two of 16.  E4M3: up to the prompt kernel's row tile, as
-// that one has all visible pages unpacked first.  fp32: always, there is no other.
+// group).  fp32: always, there is no other.  Both kernels, us, pages from HBM, groups of
+// 8, d = 128, pages of 16; A: 16 sequences of 4096 tokens, window 1024 and 16 sinks, B:
+// the same with every token visible, C: 64 sequences of 2048, every token visible:
+//   f16, rows          8           16          24          40          96
+//   A  few | prompt    12 | 17     21 | 18     18 | 18     21 | 19     30 | 21
+//   B  few | prompt    28 | 34     41 | 35     39 | 35     51 | 36     91 | 38
+//   C  few | prompt    47 | 63     48 | 65     77 | 65     95 | 66    173 | 66
+//   E4M3, rows        16           40          64          96         128
+//   A  few | prompt    25 | 31     22 | 32     25 | 33     30 | 34     49 | 35
+//   B  few | prompt    38 | 76     47 | 77     67 | 77     82 | 78    128 | 79
+//   C  few | prompt    39 | 140    87 | 140   112 | 141   159 | 141   201 | 142
+// 16-bit: one row tile of the few-rows kernel.  At 16 rows neither is always the faster
+// one; up to 8 the few-rows kernel is, from 24 on hardly ever (d = 64: 24 rows of A 12
+// and 14 us).  E4M3: the prompt kernel has all visible pages unpacked first, into a
+// workspace that calls of up to 128 rows are promised not to need; it is up to 1.6 times
+// as fast at the upper end of these.
 bool window_few_rows(qasa_dtype dt, long long rows) {
     return dt == QASA_DTYPE_F32 || rows <= (dt == QASA_DTYPE_E4M3 ? 128 : 16);
 }
