@@ -151,8 +151,9 @@ qasa_status qasa_kv_append(const qasa_kv_cache *cache, const int32_t *block_tabl
  * Pair i (i < rot_dim / 2) is channels (i, i + rot_dim / 2), or with
  * `interleaved` channels (2i, 2i + 1); channels >= rot_dim stay as they are.  A
  * rotated value is rounded once: to the cache dtype (f16 for the queries of an
- * E4M3 cache), or to the page's E4M3 code.  The box holds the min / max of the
- * keys as stored.
+ * E4M3 cache), or to the page's E4M3 code (a value next to the border of two codes
+ * may get the other one than 64-bit arithmetic would give it, one step apart).  The
+ * box holds the min / max of the keys as stored.
  */
 typedef struct {
     const float *table;        /* device, [max_positions][2][rot_dim / 2]: a row of cosines, a row of sines */
@@ -308,8 +309,11 @@ qasa_status qasa_dense_decode_attention(const qasa_kv_cache *cache, const void *
  * non-NULL, else max_q_tokens.  Query t is at position i = seq_lens[b] - n_b + t
  * and sees the tokens j <= i with j < sink_tokens or j > i - window:
  *     out = sum_j softmax_j(scale * q.k_j) v_j
- * fp32 statistics and sums; scale <= 0 selects 1/sqrt(d).  A query that sees
- * nothing (a position below 0, pages that are all bad) gets zeros.
+ * Scores, statistics and sums are fp32; over 16-bit and E4M3 caches each weight is
+ * rounded to the type of q (half a step, relative) before it meets its value, as in
+ * the decode calls above, so that out carries two roundings of its type.  scale <= 0
+ * selects 1/sqrt(d).  A query that sees nothing (a position below 0, pages that are
+ * all bad) gets zeros.
  *   q, out         [batch][max_q_tokens][num_q_heads][head_dim]; rows of out at or
  *                  past n_b are left as they were
  *   window         >= 1, the query's own token included

@@ -1,5 +1,6 @@
-// window_rows.cu -- windowed attention for few query rows per KV head: the
-// decode step, and the verification of a few drafted tokens.
+// window_rows.cu -- windowed attention for few query rows (tokens x heads of the
+// group) per KV head: the decode step and, up to 16 rows, drafted tokens; E4M3 up to
+// 128 rows, as their pages need no unpacking here; every fp32 call.
 //
 //   out(i) = sum_j softmax_j(scale q_i . k_j) v_j  over  j <= i, j < sinks or j > i - window
 //
