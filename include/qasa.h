@@ -85,6 +85,8 @@ typedef enum {
 #define QASA_DEVERR_APPEND    0x10 /* append_lens[b] (q_lens[b]) outside [0, max_new_tokens (max_q_tokens)]: clamped */
 #define QASA_DEVERR_SELECTED  0x20 /* a selected id outside [0, N_b): page skipped */
 #define QASA_DEVERR_POSITION  0x40 /* a token's position is beyond the rotation table: token skipped */
+#define QASA_DEVERR_PARENT    0x80 /* a parent that is no earlier drafted token (no sequence of the batch): none taken */
+#define QASA_DEVERR_KEEP      0x100 /* kept tokens that do not ascend or lie beyond the sequence: list cut there */
 
 typedef struct {
     void *k_pool;            /* [num_phys_pages][num_kv_heads][page_size][head_dim] */
@@ -193,6 +195,92 @@ qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotati
                                    const qasa_token_rows *k_new, const qasa_token_rows *v_new,
                                    int32_t batch, int32_t max_new_tokens, int32_t *device_status,
                                    cudaStream_t stream);
+
+/*
+ * The rotating append with the positions of the new tokens given, for tokens whose
+ * position is not that of their slot: a tree of drafted tokens (siblings share a
+ * position), image and video tokens (a position in time, height and width, some
+ * channel pairs turning by each).  Channel pair i of token (b, t) turns by entry i of
+ * the table's row
+ *     data[pair_axes[i] * axis_stride + b * batch_stride + t]
+ * Everything else is as in qasa_kv_append_rotated: token t goes to the slot of position
+ * seq_lens[b] + t.  A token with a position outside [0, max_positions) on any axis is
+ * skipped, q included, its slot left as it was, and sets QASA_DEVERR_POSITION.
+ */
+typedef struct {
+    const int32_t *data;       /* device */
+    int64_t axis_stride;       /* in elements, not negative (0: all axes read the same positions) */
+    int64_t batch_stride;      /* in elements, not negative (0: all sequences have the same) */
+    int32_t num_axes;          /* 1..3 */
+    const uint8_t *pair_axes;  /* HOST, rot_dim / 2 entries below num_axes; NULL: every pair is on axis 0 */
+} qasa_positions;
+
+qasa_status qasa_kv_append_positioned(const qasa_kv_cache *cache, const qasa_rotation *rotation,
+                                      const qasa_positions *positions, const int32_t *block_table,
+                                      int32_t max_pages_per_seq, const int32_t *seq_lens,
+                                      const int32_t *append_lens, const qasa_token_rows *q,
+                                      int32_t num_q_heads, void *q_out, const qasa_token_rows *k_new,
+                                      const qasa_token_rows *v_new, int32_t batch, int32_t max_new_tokens,
+                                      int32_t *device_status, cudaStream_t stream);
+
+/*
+ * Tokens that stay move together behind a start, the others are given up: the accepted
+ * path of a tree of drafted tokens, or any part of a sequence.  Token starts[b] + keep[b][i]
+ * goes to position starts[b] + i, for i < n_b, n_b = keep_lens[b] if keep_lens is non-NULL,
+ * else max_keep; the sequence then has starts[b] + n_b tokens.
+ *   seq_lens       [batch] int32, lengths BEFORE the call (not modified)
+ *   starts         [batch] int32 in [0, seq_lens[b]] (else clamped: QASA_DEVERR_SEQ_LEN)
+ *   keep           [batch][max_keep] int32, strictly ascending from 0 on, below
+ *                  seq_lens[b] - starts[b]; NULL where max_keep is 0.  A list that breaks
+ *                  this is cut there and sets QASA_DEVERR_KEEP.
+ *   lens_out       [batch] int32 out: the new lengths, or NULL; must not overlap an input
+ * Keys and values move as they are (rotated by the positions that they had).  The box of
+ * every page from the start's on that then holds tokens (of the start's page only if it
+ * does) is taken anew from all its tokens, so that tokens given up leave it.  E4M3: amax
+ * of such a page becomes the largest of what it was and the |value| (code * s, fp32) of
+ * the tokens that come from other pages; where it grows the page's codes are
+ * re-quantised as by an append, and tokens from other pages are stored as
+ * code(code * s_src / s_new).  Slots behind the last token are left as they were.
+ * A token whose page has a bad block-table entry is not moved (QASA_DEVERR_PAGE_ID): its
+ * new slot, if that has a page, keeps what it held.  Pages that the call writes must belong
+ * to one sequence only.
+ */
+qasa_status qasa_kv_keep_tokens(const qasa_kv_cache *cache, const int32_t *block_table,
+                                int32_t max_pages_per_seq, const int32_t *seq_lens, const int32_t *starts,
+                                const int32_t *keep, int32_t max_keep, const int32_t *keep_lens,
+                                int32_t *lens_out, int32_t batch, int32_t *device_status,
+                                cudaStream_t stream);
+
+/*
+ * Copy whole pages inside the pools: K, V, boxes and scales of physical page
+ * src_pages[i] become those of dst_pages[i], for i < num_pairs (a part-filled page made a
+ * sequence's own before it is written, a pool put in order).  A pair with an id outside
+ * the pool is skipped (QASA_DEVERR_PAGE_ID).  No page may be written twice, or be both
+ * read and written, except as its own copy.
+ */
+qasa_status qasa_kv_copy_pages(const qasa_kv_cache *cache, const int32_t *src_pages, const int32_t *dst_pages,
+                               int32_t num_pairs, int32_t *device_status, cudaStream_t stream);
+
+/*
+ * Fork sequences (several answers to one prompt, the beams of a search): child c goes on
+ * from sequence r = parents[c], L = seq_lens[r].  Its block-table row gets the parent's
+ * floor(L / page_size) full pages, which both then share, and if L is not a multiple of
+ * page_size the page new_pages[c], into which the parent's part-filled page is copied:
+ * its first L % page_size slots of K and V, boxes and scales; a negative new_pages[c]
+ * takes over the parent's own page instead (for one child, where the parent ends).
+ *   parents, new_pages  [num_children] int32
+ *   table_out      [num_children][max_pages_per_seq] int32; entries behind those pages
+ *                  are left as they were
+ *   lens_out       [num_children] int32 out: L, or NULL
+ * table_out and lens_out must not overlap an input.  A child with a parent outside
+ * [0, batch) (QASA_DEVERR_PARENT), or one that needs a page and has a bad one, or whose
+ * parent's is bad (QASA_DEVERR_PAGE_ID), is skipped: its row and length stay as they were.
+ * New pages must differ from each other and from the pages that are read.
+ */
+qasa_status qasa_kv_fork(const qasa_kv_cache *cache, const int32_t *block_table, int32_t max_pages_per_seq,
+                         const int32_t *seq_lens, int32_t batch, const int32_t *parents,
+                         const int32_t *new_pages, int32_t num_children, int32_t *table_out,
+                         int32_t *lens_out, int32_t *device_status, cudaStream_t stream);
 
 /*
  * Rebuild the page boxes of whole sequences from the keys already in k_pool:
@@ -344,6 +432,56 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
                                   const int32_t *seq_lens, int32_t window, int32_t sink_tokens,
                                   float scale, void *out, void *workspace, size_t workspace_bytes,
                                   int32_t batch, int32_t *device_status, cudaStream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache: several continuations of
+ * every sequence verified at once.  The newest n_b tokens of sequence b are drafted ones
+ * (n_b = q_lens[b] if q_lens is non-NULL, else max_q_tokens), whose keys and values are
+ * in the cache behind a context of ctx_b = seq_lens[b] - n_b tokens, and the queries are
+ * theirs.  Query t sees the drafted tokens j < n_b whose bit is set in its mask row (its
+ * own token only if its own bit is set), and of the context what a token depth_t + 1
+ * tokens behind it sees through the window and the sinks:
+ *     j < ctx_b with j < sink_tokens or j > ctx_b + depth_t - window
+ * where depth_t is the number of drafted tokens that it sees minus one (0 for none):
+ * its depth in the tree.  Among the drafted tokens the mask alone decides.
+ *   q, out         as in qasa_window_attention; rows of out at or past n_b are left as
+ *                  they were
+ *   mask           [batch][max_q_tokens][W] 32-bit words, W = ceil(max_q_tokens / 32):
+ *                  bit j % 32 of word j / 32 of row t; bits at or past n_b, and rows, are
+ *                  not looked at
+ *   mask_batch_stride  words from one sequence's mask to the next, at least
+ *                  max_q_tokens * W, or 0: all sequences share one
+ *   workspace      device memory of qasa_tree_workspace_size bytes, 16-byte aligned
+ *                  (scratch, no initialisation; NULL where that is 0).  Memory for a larger
+ *                  batch, max_q_tokens and max_pages_per_seq serves every smaller call.
+ * max_q_tokens up to 1024, any group size 1..8.  Precision, scale, bad pages, NaN
+ * queries and QASA_DEVERR_TIMEOUT as in qasa_window_attention; a query that sees
+ * nothing gets zeros.  Keys and values must be finite of the context's tokens that a
+ * query at depth 0 sees and of the drafted tokens that some query sees; other slots
+ * may hold anything.
+ */
+size_t qasa_tree_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
+                                int32_t max_q_tokens, int32_t max_pages_per_seq);
+qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
+                                int32_t max_q_tokens, const int32_t *q_lens, const int32_t *mask,
+                                int64_t mask_batch_stride, const int32_t *block_table,
+                                int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t window,
+                                int32_t sink_tokens, float scale, void *out, void *workspace,
+                                size_t workspace_bytes, int32_t batch, int32_t *device_status,
+                                cudaStream_t stream);
+
+/*
+ * Mask rows and depths of trees given by their parents: token t < n_b (n_b = lens[b], or
+ * max_tokens) hangs below token parents[b][t] < t, or -1 directly below the context; it
+ * sees itself and the tokens above it, and its depth is their number.
+ *   parents        [batch][max_tokens] int32; an entry outside [-1, t) counts as -1 and
+ *                  sets QASA_DEVERR_PARENT
+ *   mask           [batch][max_tokens][W] out, as qasa_tree_attention takes it
+ *   depths         [batch][max_tokens] int32 out, or NULL
+ * Rows at or past n_b are left as they were.  max_tokens up to 1024.
+ */
+qasa_status qasa_tree_masks(const int32_t *parents, int32_t batch, int32_t max_tokens, const int32_t *lens,
+                            int32_t *mask, int32_t *depths, int32_t *device_status, cudaStream_t stream);
 
 /* Bytes of the fixed device buffer that qasa_sparse_decode_attention_noalloc
  * uses in place of a workspace (held by every device that loads the library). */

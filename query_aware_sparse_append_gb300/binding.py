@@ -32,6 +32,8 @@ DEVERR = {
     0x10: "append length out of range",
     0x20: "selected id out of range",
     0x40: "position beyond the rotation table",
+    0x80: "parent out of range",
+    0x100: "kept tokens not ascending within the sequence",
 }
 
 
@@ -50,6 +52,11 @@ class _Rotation(ctypes.Structure):
 
 class _TokenRows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class _Positions(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("axis_stride", ctypes.c_int64), ("batch_stride", ctypes.c_int64),
+                ("num_axes", ctypes.c_int32), ("pair_axes", ctypes.c_char_p)]
 
 
 _ThreeRows = ctypes.c_int64 * 9      # three qasa_token_rows, filled at once
@@ -79,6 +86,21 @@ _lib.qasa_sparse_decode_attention_noalloc.argtypes = [_C, _P, _I, _P, _I, _P, _P
 _lib.qasa_sparse_decode_attention_noalloc.restype = _I
 _lib.qasa_kv_append_rotated.argtypes = [_C, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _I, _P, _P]
 _lib.qasa_kv_append_rotated.restype = _I
+_lib.qasa_kv_append_positioned.argtypes = [_C, _P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _I, _P, _P]
+_lib.qasa_kv_append_positioned.restype = _I
+_lib.qasa_kv_keep_tokens.argtypes = [_C, _P, _I, _P, _P, _P, _I, _P, _P, _I, _P, _P]
+_lib.qasa_kv_keep_tokens.restype = _I
+_lib.qasa_kv_copy_pages.argtypes = [_C, _P, _P, _I, _P, _P]
+_lib.qasa_kv_copy_pages.restype = _I
+_lib.qasa_kv_fork.argtypes = [_C, _P, _I, _P, _I, _P, _P, _I, _P, _P, _P, _P]
+_lib.qasa_kv_fork.restype = _I
+_lib.qasa_tree_workspace_size.argtypes = [_I, _I, _C, _I, _I]
+_lib.qasa_tree_workspace_size.restype = ctypes.c_size_t
+_lib.qasa_tree_attention.argtypes = [_C, _P, _I, _I, _P, _P, ctypes.c_int64, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P,
+                                     ctypes.c_size_t, _I, _P, _P]
+_lib.qasa_tree_attention.restype = _I
+_lib.qasa_tree_masks.argtypes = [_P, _I, _I, _P, _P, _P, _P, _P]
+_lib.qasa_tree_masks.restype = _I
 _lib.qasa_window_workspace_size.argtypes = [_I, _I, _C, _I, _I, _I, _I]
 _lib.qasa_window_workspace_size.restype = ctypes.c_size_t
 _lib.qasa_window_attention.argtypes = [_C, _P, _I, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t,
@@ -110,7 +132,8 @@ EXPORTED = ("qasa_kv_append", "qasa_decode_workspace_size", "qasa_select_pages",
             "qasa_rebuild_page_bounds", "qasa_page_attention_mass", "qasa_page_hit_rate",
             "qasa_host_decode_workspace_size", "qasa_sparse_decode_attention_host",
             "qasa_host_call_is_direct", "qasa_kv_append_rotated", "qasa_window_workspace_size",
-            "qasa_window_attention", "qasa_status_string", "qasa_version",
+            "qasa_window_attention", "qasa_kv_append_positioned", "qasa_kv_keep_tokens", "qasa_kv_copy_pages",
+            "qasa_kv_fork", "qasa_tree_workspace_size", "qasa_tree_attention", "qasa_tree_masks", "qasa_status_string", "qasa_version",
             "qasa_debug_trace_bytes", "qasa_debug_trace")
 
 # trace buffer layout (include/qasa.h)
@@ -326,6 +349,14 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
         with torch.cuda.device(index):
             return kv_append_rotated(cache, block_table, seq_lens, k_new, v_new, table, q, q_out, append_lens,
                                      interleaved, status, stream)
+    return _append_rotated(cache, block_table, seq_lens, k_new, v_new, table, q, q_out, append_lens, interleaved, None, status,
+                           stream)
+
+
+def _append_rotated(cache, block_table, seq_lens, k_new, v_new, table, q, q_out, append_lens, interleaved, given, status,
+                    stream):
+    """The rotating append on the cache's device, the current one; `given`: (positions, pair_axes) or None."""
+    index = cache.device_index
     value, d = cache.value_dtype, cache.head_dim
     kr = _token_rows(k_new, "k_new", value, d, index)
     vr = _token_rows(v_new, "v_new", value, d, index)
@@ -356,13 +387,139 @@ def kv_append_rotated(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: 
         raise ValueError("the cache must be on a CUDA device")
     rows = _ThreeRows(*kr, *vr, *qr)
     at = ctypes.addressof(rows)
-    code = _lib.qasa_kv_append_rotated(
-        cache.c_ref, ctypes.byref(rot), _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
+    args = (
+        _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
         _arg(seq_lens, "seq_lens", torch.int32, (B,), index), _arg(append_lens, "append_lens", torch.int32, (B,), index),
         None if q is None else at + 48, hq, out, at, at + 24, B, T, _status_arg(status, index), _call_stream(stream, index))
+    if given is None:
+        code = _lib.qasa_kv_append_rotated(cache.c_ref, ctypes.byref(rot), *args)
+        if code:
+            _check(code, "qasa_kv_append_rotated")
+        return q_out
+    pos = _positions(*given, B, T, half, index)
+    code = _lib.qasa_kv_append_positioned(cache.c_ref, ctypes.byref(rot), ctypes.byref(pos), *args)
     if code:
-        _check(code, "qasa_kv_append_rotated")
+        _check(code, "qasa_kv_append_positioned")
     return q_out
+
+
+def _positions(positions: torch.Tensor, axes, B: int, T: int, half: int, index: int) -> _Positions:
+    shape = positions.shape
+    num = shape[0] if len(shape) == 3 else 1
+    if len(shape) not in (2, 3) or positions.dtype is not torch.int32 or positions.get_device() != index \
+            or shape[-1] != T or shape[-2] not in (1, B) or (T > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be an int32 tensor [axes, batch or 1, tokens] or [batch or 1, tokens] on cuda:%d, "
+                         "its tokens contiguous" % index)
+    if not 1 <= num <= 3:
+        raise ValueError("positions must have one to three axes")
+    if axes is not None:
+        if len(axes) != half or not all(0 <= a < num for a in axes):
+            raise ValueError("pair_axes must hold an axis of positions for each of the table's pairs")
+        axes = bytes(axes)
+    return _Positions(positions.data_ptr(), positions.stride(0) if len(shape) == 3 else 0,
+                      positions.stride(-2) if shape[-2] > 1 else 0, num, axes)
+
+
+def kv_append_positioned(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Tensor, k_new: torch.Tensor,
+                         v_new: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, q: Optional[torch.Tensor] = None,
+                         q_out: Optional[torch.Tensor] = None, append_lens: Optional[torch.Tensor] = None,
+                         pair_axes: Optional[Sequence[int]] = None, interleaved: bool = False,
+                         status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """kv_append_rotated with the positions of the new tokens given, int32 [B, T] or [axes, B, T] (B or 1, up to
+    three axes): a tree's tokens turn by their depth behind the context, image tokens by their time, height and
+    width.  pair_axes: the axis of each of the table's channel pairs (None: the first); see pair_sections.  The
+    tokens still go to the slots after seq_lens."""
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return kv_append_positioned(cache, block_table, seq_lens, k_new, v_new, table, positions, q, q_out, append_lens,
+                                        pair_axes, interleaved, status, stream)
+    return _append_rotated(cache, block_table, seq_lens, k_new, v_new, table, q, q_out, append_lens, interleaved,
+                           (positions, pair_axes), status, stream)
+
+
+def pair_sections(sections: Sequence[int]) -> list:
+    """pair_axes of channel pairs in one span per axis, of these numbers of pairs."""
+    return [axis for axis, n in enumerate(sections) for _ in range(n)]
+
+
+def kv_keep_tokens(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Tensor, starts: torch.Tensor,
+                   keep: torch.Tensor, keep_lens: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Of the tokens from starts[b] on, keep[b, :keep_lens[b]] (default: all of keep [B, M], ascending, counted from
+    the start) stay and move together behind the start; the others are given up.  Boxes and E4M3 scales follow.
+    Returns the new lengths [B] (lens_out, allocated on the call's stream where not given)."""
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return kv_keep_tokens(cache, block_table, seq_lens, starts, keep, keep_lens, lens_out, status, stream)
+    if block_table.dim() != 2 or keep.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages_per_seq] and keep [batch, tokens]")
+    B, M = keep.shape
+    maxp = block_table.shape[1]
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    if lens_out is None:
+        with _allocating_on(stream):
+            lens_out = torch.empty(B, dtype=torch.int32, device=cache.k_pool.device)
+    code = _lib.qasa_kv_keep_tokens(
+        cache.c_ref, _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), _arg(starts, "starts", torch.int32, (B,), index),
+        _arg(keep, "keep", torch.int32, (B, M), index), M, _arg(keep_lens, "keep_lens", torch.int32, (B,), index),
+        _arg(lens_out, "lens_out", torch.int32, (B,), index), B, _status_arg(status, index), _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_kv_keep_tokens")
+    return lens_out
+
+
+def kv_copy_pages(cache: PagedKVCache, src_pages: torch.Tensor, dst_pages: torch.Tensor,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Physical pages src_pages [n] become those of dst_pages [n]: K, V, boxes and scales."""
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return kv_copy_pages(cache, src_pages, dst_pages, status, stream)
+    if src_pages.dim() != 1:
+        raise ValueError("src_pages must be [pairs]")
+    n = src_pages.shape[0]
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    code = _lib.qasa_kv_copy_pages(cache.c_ref, _arg(src_pages, "src_pages", torch.int32, (n,), index),
+                                   _arg(dst_pages, "dst_pages", torch.int32, (n,), index), n, _status_arg(status, index),
+                                   _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_kv_copy_pages")
+
+
+def kv_fork(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
+            new_pages: torch.Tensor, table_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+            status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Children go on from sequences parents [C]: (table_out [C, max_pages_per_seq], lens_out [C]).  Full pages are
+    shared; a part-filled one is copied into new_pages[c], or taken over where that is negative.  Entries of table_out
+    behind a child's pages are left as they were (-1 where it is allocated here, on the call's stream)."""
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return kv_fork(cache, block_table, seq_lens, parents, new_pages, table_out, lens_out, status, stream)
+    if block_table.dim() != 2 or parents.dim() != 1:
+        raise ValueError("block_table must be [batch, max_pages_per_seq] and parents [children]")
+    (B, maxp), C = block_table.shape, parents.shape[0]
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    if table_out is None or lens_out is None:
+        with _allocating_on(stream):
+            if table_out is None:
+                table_out = torch.full((C, maxp), -1, dtype=torch.int32, device=cache.k_pool.device)
+            if lens_out is None:
+                lens_out = torch.zeros(C, dtype=torch.int32, device=cache.k_pool.device)
+    code = _lib.qasa_kv_fork(
+        cache.c_ref, _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), B, _arg(parents, "parents", torch.int32, (C,), index),
+        _arg(new_pages, "new_pages", torch.int32, (C,), index), C, _arg(table_out, "table_out", torch.int32, (C, maxp), index),
+        _arg(lens_out, "lens_out", torch.int32, (C,), index), _status_arg(status, index), _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_kv_fork")
+    return table_out, lens_out
 
 
 NO_WINDOW = 0x7FFFFFFF      # a window that every token is in
@@ -427,6 +584,91 @@ def window_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Te
         _status_arg(status, index), _call_stream(stream, index))
     if code:
         _check(code, "qasa_window_attention")
+    return out
+
+
+def tree_masks(parents: torch.Tensor, lens: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+               depths: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Mask rows [B, T, ceil(T / 32)] and depths [B, T] (int32) of trees of drafted tokens given by parents [B, T]
+    (an earlier token, or -1: the context).  Rows at or past lens[b] (default T) are left as they were (0 where they
+    are allocated here, on the call's stream)."""
+    index = parents.get_device()
+    if index < 0:
+        raise ValueError("parents must be on a CUDA device")
+    if _get_device() != index:
+        with torch.cuda.device(index):
+            return tree_masks(parents, lens, mask, depths, status, stream)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [batch, tokens]")
+    B, T = parents.shape
+    W = -(-T // 32)
+    if mask is None or depths is None:
+        with _allocating_on(stream):
+            if mask is None:
+                mask = torch.zeros((B, T, W), dtype=torch.int32, device=parents.device)
+            if depths is None:
+                depths = torch.zeros((B, T), dtype=torch.int32, device=parents.device)
+    code = _lib.qasa_tree_masks(
+        _arg(parents, "parents", torch.int32, (B, T), index), B, T, _arg(lens, "lens", torch.int32, (B,), index),
+        _arg(mask, "mask", torch.int32, (B, T, W), index), _arg(depths, "depths", torch.int32, (B, T), index),
+        _status_arg(status, index), _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_tree_masks")
+    return mask, depths
+
+
+def alloc_tree_workspace(cache: PagedKVCache, batch: int, num_q_heads: int, max_q_tokens: int,
+                         max_pages_per_seq: int) -> torch.Tensor:
+    """Workspace of tree_attention calls of up to this batch, these tokens and pages."""
+    n = int(_lib.qasa_tree_workspace_size(batch, num_q_heads, cache.c_ref, max_q_tokens, max_pages_per_seq))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_pool.device)
+
+
+def tree_attention(cache: PagedKVCache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                   mask: torch.Tensor, q_lens: Optional[torch.Tensor] = None, window: Optional[int] = None,
+                   sink_tokens: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of a tree of drafted tokens: q [B, T, Hq, d] holds the queries of the last q_lens[b] (default T) of
+    seq_lens[b] tokens.  Query t sees the drafted tokens of its row of mask (int32 words [B or 1, T, ceil(T / 32)], as
+    tree_masks makes them) and of the context before them its window (None: everything) and the first sink_tokens.
+    Rows at or past q_lens[b] of `out` are left as they were (unset where it is allocated here, on the call's
+    stream)."""
+    index = cache.device_index
+    if index >= 0 and _get_device() != index:
+        with torch.cuda.device(index):
+            return tree_attention(cache, q, block_table, seq_lens, mask, q_lens, window, sink_tokens, scale, out, workspace,
+                                  status, stream)
+    shape = q.shape
+    if len(shape) != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [batch, tokens, heads, head_dim] and block_table [batch, max_pages_per_seq]")
+    B, T, hq, d = shape
+    if d != cache.head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    value, maxp, W = cache.value_dtype, block_table.shape[1], -(-T // 32)
+    if mask.dim() != 3 or mask.shape[0] not in (1, B):
+        raise ValueError("mask must be [batch or 1, tokens, words]")
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    qp = _arg(q, "q", value, shape, index)
+    if out is None or workspace is None:
+        with _allocating_on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = alloc_tree_workspace(cache, B, hq, T, maxp)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous memory on cuda:%d" % index)
+    code = _lib.qasa_tree_attention(
+        cache.c_ref, qp, hq, T, _arg(q_lens, "q_lens", torch.int32, (B,), index),
+        _arg(mask, "mask", torch.int32, (mask.shape[0], T, W), index), T * W if mask.shape[0] > 1 else 0,
+        _arg(block_table, "block_table", torch.int32, (B, maxp), index), maxp,
+        _arg(seq_lens, "seq_lens", torch.int32, (B,), index), _tokens(window), _tokens(sink_tokens), scale or 0.0,
+        _arg(out, "out", value, shape, index), workspace.data_ptr(), workspace.nbytes, B, _status_arg(status, index),
+        _call_stream(stream, index))
+    if code:
+        _check(code, "qasa_tree_attention")
     return out
 
 

@@ -17,6 +17,7 @@ namespace {
 constexpr int kMaxPagesPerSeq = 16384;
 constexpr int kMaxBatch = 8192;
 constexpr int kMaxQueryTokens = 65536;
+constexpr int kMaxTreeTokens = 1024;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr int kAttnUnitWeight = 4;
 
@@ -466,6 +467,111 @@ int window_cluster(qasa_dtype dt, int rows, long long units, long long tiles) {
     return c < 1 ? 1 : c > 8 ? 8 : (int)c;
 }
 
+// The rotating append; `given`: positions of the caller, or NULL.
+qasa_status append_rotated(const qasa_kv_cache *cache, const qasa_rotation *rotation, const qasa_positions *given,
+                           const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+                           const int32_t *append_lens, const qasa_token_rows *q, int32_t num_q_heads, void *q_out,
+                           const qasa_token_rows *k_new, const qasa_token_rows *v_new, int32_t batch,
+                           int32_t max_new_tokens, int32_t *device_status, cudaStream_t stream) {
+    qasa_status st = check_cache(cache);
+    if (st != QASA_OK) return st;
+    if (!rotation) return QASA_ERR_NULL;
+    if (rotation->rot_dim < 16 || rotation->rot_dim % 16 || rotation->rot_dim > cache->head_dim ||
+        rotation->max_positions < 1 || (rotation->interleaved != 0 && rotation->interleaved != 1))
+        return QASA_ERR_SHAPE;
+    RotatedParams p = {};
+    if (given) {
+        if (given->num_axes < 1 || given->num_axes > 3 || given->axis_stride < 0 || given->batch_stride < 0)
+            return QASA_ERR_SHAPE;
+        for (int i = 0; given->pair_axes && i < rotation->rot_dim / 2; ++i) {
+            if (given->pair_axes[i] >= given->num_axes) return QASA_ERR_SHAPE;
+            p.pair_axes[i >> 4] |= (uint32_t)given->pair_axes[i] << (2 * (i & 15));
+        }
+    }
+    if (batch == 0 || max_new_tokens == 0) return QASA_OK;
+    if (given && !given->data) return QASA_ERR_NULL;
+    if (!rotation->table || !block_table || !seq_lens || !k_new || !v_new || !k_new->data || !v_new->data)
+        return QASA_ERR_NULL;
+    if (q && (!q->data || !q_out)) return QASA_ERR_NULL;
+    if (batch < 0 || batch > 65535 || max_new_tokens < 0 || max_pages_per_seq < 1 ||
+        max_pages_per_seq > kMaxPagesPerSeq)
+        return QASA_ERR_SHAPE;
+    if (q && num_q_heads < 1) return QASA_ERR_SHAPE;
+    const long long per16 = 16 / (cache->dtype == QASA_DTYPE_F32 ? 4 : 2);   // elements of an input in 16 bytes
+    const qasa_token_rows *rows[3] = {k_new, v_new, q};
+    for (const qasa_token_rows *r : rows) {
+        if (!r) continue;
+        if (!aligned16(r->data)) return QASA_ERR_ALIGN;
+        if (batch > 1 && r->batch_stride < 0) return QASA_ERR_SHAPE;
+        if (max_new_tokens > 1 && r->token_stride < 0) return QASA_ERR_SHAPE;
+        if (batch > 1 && r->batch_stride % per16) return QASA_ERR_ALIGN;
+        if (max_new_tokens > 1 && r->token_stride % per16) return QASA_ERR_ALIGN;
+    }
+    if (!aligned16(rotation->table) || (q && !aligned16(q_out))) return QASA_ERR_ALIGN;
+    const void *words[] = {block_table, seq_lens, append_lens, device_status, given ? given->data : nullptr};
+    for (const void *w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
+    p.positions = given ? given->data : nullptr;
+    p.pos_axis = given ? given->axis_stride : 0;
+    p.pos_batch = given ? given->batch_stride : 0;
+    p.num_axes = given ? given->num_axes : 0;
+    p.k_pool = cache->k_pool;
+    p.v_pool = cache->v_pool;
+    p.bounds = cache->page_bounds;
+    p.scales = cache->page_scales;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.append_lens = append_lens;
+    p.table = rotation->table;
+    p.q = q ? q->data : nullptr;
+    p.q_out = q ? q_out : nullptr;
+    p.k_new = k_new->data;
+    p.v_new = v_new->data;
+    p.q_batch = q ? q->batch_stride : 0;
+    p.q_token = q ? q->token_stride : 0;
+    p.k_batch = k_new->batch_stride;
+    p.k_token = k_new->token_stride;
+    p.v_batch = v_new->batch_stride;
+    p.v_token = v_new->token_stride;
+    p.status = device_status;
+    p.num_phys = cache->num_phys_pages;
+    p.Hkv = cache->num_kv_heads;
+    p.Hq = q ? num_q_heads : 0;
+    p.P = cache->page_size;
+    p.max_pages = max_pages_per_seq;
+    p.T = max_new_tokens;
+    p.max_positions = rotation->max_positions;
+    p.rot = rotation->rot_dim;
+    p.interleaved = rotation->interleaved;
+    p.kv_blocks = 0;
+    p.q_span = 1;
+    p.sms = sm_count() > 0 ? sm_count() : 1;
+    const cudaError_t e = launch_append_rotated(cache->dtype, cache->head_dim, p, batch, stream);
+    if (e == cudaErrorInvalidConfiguration) return QASA_ERR_SHAPE;
+    return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+// Whether the two stretches of memory have a byte in common (NULL: none).
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x && y && na && nb && x < y + nb && y < x + na;
+}
+
+PageCopyParams page_copy(const qasa_kv_cache *c, int32_t *status) {
+    PageCopyParams p = {};
+    p.k_pool = c->k_pool;
+    p.v_pool = c->v_pool;
+    p.bounds = c->page_bounds;
+    p.scales = c->dtype == QASA_DTYPE_E4M3 ? c->page_scales : nullptr;
+    p.status = status;
+    p.num_phys = c->num_phys_pages;
+    p.Hkv = c->num_kv_heads;
+    p.P = c->page_size;
+    p.row_chunks = (int)(c->head_dim * elem_size(c->dtype) / 16);
+    p.pieces = page_pieces(p);
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -511,69 +617,112 @@ qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotati
                                    const qasa_token_rows *k_new, const qasa_token_rows *v_new,
                                    int32_t batch, int32_t max_new_tokens, int32_t *device_status,
                                    cudaStream_t stream) {
-    qasa_status st = check_cache(cache);
-    if (st != QASA_OK) return st;
-    if (!rotation) return QASA_ERR_NULL;
-    if (rotation->rot_dim < 16 || rotation->rot_dim % 16 || rotation->rot_dim > cache->head_dim ||
-        rotation->max_positions < 1 || (rotation->interleaved != 0 && rotation->interleaved != 1))
-        return QASA_ERR_SHAPE;
-    if (batch == 0 || max_new_tokens == 0) return QASA_OK;
-    if (!rotation->table || !block_table || !seq_lens || !k_new || !v_new || !k_new->data || !v_new->data)
-        return QASA_ERR_NULL;
-    if (q && (!q->data || !q_out)) return QASA_ERR_NULL;
-    if (batch < 0 || batch > 65535 || max_new_tokens < 0 || max_pages_per_seq < 1 ||
-        max_pages_per_seq > kMaxPagesPerSeq)
-        return QASA_ERR_SHAPE;
-    if (q && num_q_heads < 1) return QASA_ERR_SHAPE;
-    const long long per16 = 16 / (cache->dtype == QASA_DTYPE_F32 ? 4 : 2);   // elements of an input in 16 bytes
-    const qasa_token_rows *rows[3] = {k_new, v_new, q};
-    for (const qasa_token_rows *r : rows) {
-        if (!r) continue;
-        if (!aligned16(r->data)) return QASA_ERR_ALIGN;
-        if (batch > 1 && r->batch_stride < 0) return QASA_ERR_SHAPE;
-        if (max_new_tokens > 1 && r->token_stride < 0) return QASA_ERR_SHAPE;
-        if (batch > 1 && r->batch_stride % per16) return QASA_ERR_ALIGN;
-        if (max_new_tokens > 1 && r->token_stride % per16) return QASA_ERR_ALIGN;
+    return append_rotated(cache, rotation, nullptr, block_table, max_pages_per_seq, seq_lens, append_lens, q, num_q_heads,
+                          q_out, k_new, v_new, batch, max_new_tokens, device_status, stream);
+}
+
+qasa_status qasa_kv_append_positioned(const qasa_kv_cache *cache, const qasa_rotation *rotation,
+                                      const qasa_positions *positions, const int32_t *block_table,
+                                      int32_t max_pages_per_seq, const int32_t *seq_lens,
+                                      const int32_t *append_lens, const qasa_token_rows *q,
+                                      int32_t num_q_heads, void *q_out, const qasa_token_rows *k_new,
+                                      const qasa_token_rows *v_new, int32_t batch, int32_t max_new_tokens,
+                                      int32_t *device_status, cudaStream_t stream) {
+    if (!positions) {
+        const qasa_status st = check_cache(cache);
+        return st != QASA_OK ? st : QASA_ERR_NULL;
     }
-    if (!aligned16(rotation->table) || (q && !aligned16(q_out))) return QASA_ERR_ALIGN;
-    const void *words[] = {block_table, seq_lens, append_lens, device_status};
+    return append_rotated(cache, rotation, positions, block_table, max_pages_per_seq, seq_lens, append_lens, q, num_q_heads,
+                          q_out, k_new, v_new, batch, max_new_tokens, device_status, stream);
+}
+
+qasa_status qasa_kv_keep_tokens(const qasa_kv_cache *cache, const int32_t *block_table,
+                                int32_t max_pages_per_seq, const int32_t *seq_lens, const int32_t *starts,
+                                const int32_t *keep, int32_t max_keep, const int32_t *keep_lens,
+                                int32_t *lens_out, int32_t batch, int32_t *device_status,
+                                cudaStream_t stream) {
+    const qasa_status st = check_cache(cache);
+    if (st != QASA_OK || batch == 0) return st;
+    if (!block_table || !seq_lens || !starts || (!keep && max_keep != 0)) return QASA_ERR_NULL;
+    if (batch < 0 || batch > kMaxBatch || max_pages_per_seq < 1 || max_pages_per_seq > kMaxPagesPerSeq || max_keep < 0 ||
+        max_keep > max_pages_per_seq * cache->page_size)
+        return QASA_ERR_SHAPE;
+    const void *words[] = {block_table, seq_lens, starts, keep, keep_lens, lens_out, device_status};
     for (const void *w : words)
         if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
-    RotatedParams p;
+    const size_t n = 4 * (size_t)batch;
+    if (overlap(lens_out, n, seq_lens, n) || overlap(lens_out, n, starts, n) || overlap(lens_out, n, keep_lens, n) ||
+        overlap(lens_out, n, keep, n * max_keep) || overlap(lens_out, n, block_table, n * max_pages_per_seq))
+        return QASA_ERR_SHAPE;
+    KeepParams p = {};
     p.k_pool = cache->k_pool;
     p.v_pool = cache->v_pool;
     p.bounds = cache->page_bounds;
     p.scales = cache->page_scales;
     p.block_table = block_table;
     p.seq_lens = seq_lens;
-    p.append_lens = append_lens;
-    p.table = rotation->table;
-    p.q = q ? q->data : nullptr;
-    p.q_out = q ? q_out : nullptr;
-    p.k_new = k_new->data;
-    p.v_new = v_new->data;
-    p.q_batch = q ? q->batch_stride : 0;
-    p.q_token = q ? q->token_stride : 0;
-    p.k_batch = k_new->batch_stride;
-    p.k_token = k_new->token_stride;
-    p.v_batch = v_new->batch_stride;
-    p.v_token = v_new->token_stride;
+    p.starts = starts;
+    p.keep = keep;
+    p.keep_lens = keep_lens;
+    p.lens_out = lens_out;
     p.status = device_status;
     p.num_phys = cache->num_phys_pages;
     p.Hkv = cache->num_kv_heads;
-    p.Hq = q ? num_q_heads : 0;
     p.P = cache->page_size;
     p.max_pages = max_pages_per_seq;
-    p.T = max_new_tokens;
-    p.max_positions = rotation->max_positions;
-    p.rot = rotation->rot_dim;
-    p.interleaved = rotation->interleaved;
-    p.kv_blocks = 0;
-    p.q_span = 1;
-    p.sms = sm_count() > 0 ? sm_count() : 1;
-    const cudaError_t e = launch_append_rotated(cache->dtype, cache->head_dim, p, batch, stream);
+    p.M = max_keep;
+    p.cluster = 1;
+    const cudaError_t e = launch_keep(cache->dtype, cache->head_dim, p, batch, stream);
     if (e == cudaErrorInvalidConfiguration) return QASA_ERR_SHAPE;
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+qasa_status qasa_kv_copy_pages(const qasa_kv_cache *cache, const int32_t *src_pages, const int32_t *dst_pages,
+                               int32_t num_pairs, int32_t *device_status, cudaStream_t stream) {
+    const qasa_status st = check_cache(cache);
+    if (st != QASA_OK || num_pairs == 0) return st;
+    if (!src_pages || !dst_pages) return QASA_ERR_NULL;
+    if (num_pairs < 0) return QASA_ERR_SHAPE;
+    const void *words[] = {src_pages, dst_pages, device_status};
+    for (const void *w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
+    PageCopyParams p = page_copy(cache, device_status);
+    p.src_pages = src_pages;
+    p.dst_pages = dst_pages;
+    if ((long long)num_pairs * p.pieces > 0x7fffffffLL) return QASA_ERR_SHAPE;
+    return launch_copy_pages(p, num_pairs, stream) == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+qasa_status qasa_kv_fork(const qasa_kv_cache *cache, const int32_t *block_table, int32_t max_pages_per_seq,
+                         const int32_t *seq_lens, int32_t batch, const int32_t *parents,
+                         const int32_t *new_pages, int32_t num_children, int32_t *table_out,
+                         int32_t *lens_out, int32_t *device_status, cudaStream_t stream) {
+    const qasa_status st = check_cache(cache);
+    if (st != QASA_OK || num_children == 0) return st;
+    if (!block_table || !seq_lens || !parents || !new_pages || !table_out) return QASA_ERR_NULL;
+    if (batch < 0 || batch > kMaxBatch || num_children < 0 || max_pages_per_seq < 1 || max_pages_per_seq > kMaxPagesPerSeq)
+        return QASA_ERR_SHAPE;
+    const void *words[] = {block_table, seq_lens, parents, new_pages, table_out, lens_out, device_status};
+    for (const void *w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
+    const size_t rows = 4 * (size_t)max_pages_per_seq;
+    const struct { const void *at; size_t bytes; } in[] = {{block_table, batch * rows}, {seq_lens, 4 * (size_t)batch},
+        {parents, 4 * (size_t)num_children}, {new_pages, 4 * (size_t)num_children}};
+    for (const auto &x : in)
+        if (overlap(table_out, num_children * rows, x.at, x.bytes) || overlap(lens_out, 4 * (size_t)num_children, x.at, x.bytes))
+            return QASA_ERR_SHAPE;
+    if (overlap(table_out, num_children * rows, lens_out, 4 * (size_t)num_children)) return QASA_ERR_SHAPE;
+    PageCopyParams p = page_copy(cache, device_status);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.parents = parents;
+    p.new_pages = new_pages;
+    p.table_out = table_out;
+    p.lens_out = lens_out;
+    p.max_pages = max_pages_per_seq;
+    p.batch = batch;
+    if ((long long)num_children * p.pieces > 0x7fffffffLL) return QASA_ERR_SHAPE;
+    return launch_fork(p, num_children, stream) == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 
 size_t qasa_window_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
@@ -612,7 +761,7 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
         if (!workspace || workspace_bytes < u.one || !aligned16(workspace)) return QASA_ERR_WORKSPACE;
         if (workspace_bytes / u.one < (size_t)u.group) u.group = (int)(workspace_bytes / u.one);
     }
-    WindowParams p;
+    WindowParams p = {};
     p.q = q;
     p.out = out;
     p.k_pool = cache->k_pool;
@@ -672,6 +821,83 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
     if (units * p.cluster > 0x7fffffffLL) return QASA_ERR_SHAPE;
     const cudaError_t e = launch_window_rows(cache->dtype, cache->head_dim, p, stream);
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+size_t qasa_tree_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
+                                int32_t max_q_tokens, int32_t max_pages_per_seq) {
+    (void)batch; (void)num_q_heads; (void)cache; (void)max_q_tokens; (void)max_pages_per_seq;
+    return 0;
+}
+
+qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
+                                int32_t max_q_tokens, const int32_t *q_lens, const int32_t *mask,
+                                int64_t mask_batch_stride, const int32_t *block_table,
+                                int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t window,
+                                int32_t sink_tokens, float scale, void *out, void *workspace,
+                                size_t workspace_bytes, int32_t batch, int32_t *device_status,
+                                cudaStream_t stream) {
+    qasa_status st = check_cache(cache);
+    if (st != QASA_OK) return st;
+    if (window < 1 || sink_tokens < 0 || max_q_tokens < 0 || max_q_tokens > kMaxTreeTokens) return QASA_ERR_SHAPE;
+    if (batch == 0 || max_q_tokens == 0) return QASA_OK;
+    st = check_decode(cache, q, num_q_heads, block_table, max_pages_per_seq, seq_lens, out, batch);
+    if (st != QASA_OK) return st;
+    if (!mask) return QASA_ERR_NULL;
+    const int words = (max_q_tokens + 31) / 32;
+    if (batch > 1 && mask_batch_stride != 0 && mask_batch_stride < (int64_t)max_q_tokens * words) return QASA_ERR_SHAPE;
+    const void *ints[] = {q_lens, mask, device_status};
+    for (const void *w : ints)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
+    (void)workspace; (void)workspace_bytes;
+    WindowParams p = {};
+    p.q = q;
+    p.out = out;
+    p.k_pool = cache->k_pool;
+    p.v_pool = cache->v_pool;
+    p.scales = cache->page_scales;
+    p.q_lens = q_lens;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.status = device_status;
+    p.B = batch;
+    p.T = max_q_tokens;
+    p.Hq = num_q_heads;
+    p.Hkv = cache->num_kv_heads;
+    p.G = num_q_heads / cache->num_kv_heads;
+    p.P = cache->page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_phys = cache->num_phys_pages;
+    p.window = window < 1 << 30 ? window : 1 << 30;
+    p.sinks = sink_tokens < 1 << 30 ? sink_tokens : 1 << 30;
+    const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)cache->head_dim);
+    p.scale_log2 = (float)(sc * 1.4426950408889634);
+    p.mask = mask;
+    p.mask_batch = batch > 1 ? mask_batch_stride : 0;
+    p.mask_words = words;
+    const long long tiles = most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens);
+    const long long units = (long long)batch * p.Hkv * window_row_tiles(cache->dtype, p.T * p.G);
+    p.cluster = window_cluster(cache->dtype, p.T * p.G, units, tiles);
+    if (units * p.cluster > 0x7fffffffLL) return QASA_ERR_SHAPE;
+    return launch_tree_rows(cache->dtype, cache->head_dim, p, stream) == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+}
+
+qasa_status qasa_tree_masks(const int32_t *parents, int32_t batch, int32_t max_tokens, const int32_t *lens,
+                            int32_t *mask, int32_t *depths, int32_t *device_status, cudaStream_t stream) {
+    if (batch < 0 || batch > kMaxBatch || max_tokens < 0 || max_tokens > kMaxTreeTokens) return QASA_ERR_SHAPE;
+    if (batch == 0 || max_tokens == 0) return QASA_OK;
+    if (!parents || !mask) return QASA_ERR_NULL;
+    const void *ints[] = {parents, lens, mask, depths, device_status};
+    for (const void *w : ints)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
+    TreeMaskParams p = {};
+    p.parents = parents;
+    p.lens = lens;
+    p.mask = mask;
+    p.depths = depths;
+    p.status = device_status;
+    p.T = max_tokens;
+    p.words = (max_tokens + 31) / 32;
+    return launch_tree_masks(p, batch, stream) == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 
 qasa_status qasa_rebuild_page_bounds(const qasa_kv_cache *cache, const int32_t *block_table,

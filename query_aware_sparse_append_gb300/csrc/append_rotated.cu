@@ -25,7 +25,13 @@
 // chunks (j, j + R/2) for half-split pairs, chunks (2j, 2j + 1) for neighbouring
 // pairs; either way its angles are entries [j * EPC, (j + 1) * EPC) of the table
 // row, so one addressing rule serves both.
-#include "qasa_device.cuh"
+//
+// GIVEN: the positions come from the caller, on up to three axes, each channel pair
+// turning by the position on its own axis (a tree of drafted tokens, whose siblings
+// share a position; image tokens with a time, a height and a width).  Slots still
+// follow the lengths.  A lane's pairs are EPC neighbours of the table row, mostly of
+// one axis, so it reads the rows of the axes that it has and picks.
+#include "page_rows.cuh"
 #include "qasa_launch.h"
 
 namespace qasa {
@@ -39,6 +45,7 @@ struct LanePair {
     int ca, cb;      // first channels of the two chunks
     int angle;       // first entry of the table row
     bool turns;
+    uint32_t axes;   // GIVEN: axis of each of the lane's pairs, two bits each
 };
 
 template <int EPC, bool INTER>
@@ -57,6 +64,30 @@ __device__ __forceinline__ LanePair lane_pair(int j, int rot) {
     return l;
 }
 
+// The axes of the pairs from entry `angle` of a table row on.
+template <int EPC>
+__device__ __forceinline__ uint32_t pair_axes(const RotatedParams &p, int angle) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i == angle >> 4) w = p.pair_axes[i];
+    return w >> (2 * (angle & 15)) & ((1u << (2 * EPC)) - 1u);
+}
+
+// Positions of token `tok` of sequence b on its axes; false where the table has not all of them.
+struct Given { int at[3]; };
+
+__device__ __forceinline__ bool given_positions(const RotatedParams &p, int b, int tok, Given &g) {
+    const int32_t *row = p.positions + (size_t)b * p.pos_batch + tok;
+    bool ok = true;
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+        g.at[a] = a < p.num_axes ? __ldg(row + (size_t)a * p.pos_axis) : 0;
+        ok = ok && g.at[a] >= 0 && g.at[a] < p.max_positions;
+    }
+    return ok;
+}
+
 template <int EPC> struct Angles { float c[EPC], s[EPC]; };
 
 template <int EPC>
@@ -69,6 +100,28 @@ __device__ __forceinline__ void load_angles(Angles<EPC> &a, const RotatedParams 
         const float4 s = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + e));
         a.c[e] = c.x; a.c[e + 1] = c.y; a.c[e + 2] = c.z; a.c[e + 3] = c.w;
         a.s[e] = s.x; a.s[e + 1] = s.y; a.s[e + 2] = s.z; a.s[e + 3] = s.w;
+    }
+}
+
+template <int EPC>
+__device__ __forceinline__ void load_angles(Angles<EPC> &out, const RotatedParams &p, const Given &g, const LanePair &l) {
+    if (!l.turns) return;
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+        // the lane's pairs on this axis: bit 2 e for pair e
+        const uint32_t lo = l.axes, hi = l.axes >> 1, ones = 0x55555555u & ((1u << (2 * EPC)) - 1u);
+        const uint32_t mine = (a == 0 ? ~lo & ~hi : a == 1 ? lo & ~hi : ~lo & hi) & ones;
+        if (!mine) continue;
+        const float *row = p.table + (size_t)g.at[a] * p.rot + l.angle;
+#pragma unroll
+        for (int e = 0; e < EPC; e += 4) {
+            const float4 c = __ldg(reinterpret_cast<const float4 *>(row + e));
+            const float4 s = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + e));
+            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (mine >> (2 * (e + k)) & 1u) { out.c[e + k] = cs[k]; out.s[e + k] = sn[k]; }
+        }
     }
 }
 
@@ -102,14 +155,17 @@ __device__ __forceinline__ void rotate(const uint4 &a, const uint4 &b, const Ang
 
 // The new tokens of sequence b that this call can place: positions L0 .. L0 + n.
 // `report`: this thread records what is wrong with the sequence.
+template <bool GIVEN>
 __device__ __forceinline__ int new_tokens(const RotatedParams &p, int b, int &L0, bool report) {
     L0 = p.seq_lens[b];
     int n = p.append_lens ? p.append_lens[b] : p.T, err = 0;
     if (n < 0 || n > p.T) { err |= QASA_DEVERR_APPEND; n = n < 0 ? 0 : p.T; }
     if (L0 < 0) { err |= QASA_DEVERR_SEQ_LEN; n = 0; }
-    if (n > p.max_positions - L0) {      // also keeps L0 + n inside 32 bits
-        if (n > 0) err |= QASA_DEVERR_POSITION;
-        n = max(0, p.max_positions - L0);
+    // the largest position + 1; also keeps L0 + n inside 32 bits
+    const int limit = GIVEN ? 0x7fffffff : p.max_positions;
+    if (n > limit - L0) {
+        if (n > 0) err |= GIVEN ? QASA_DEVERR_SEQ_LEN : QASA_DEVERR_POSITION;
+        n = max(0, limit - L0);
     }
     if (err && report && p.status) atomicOr(p.status, err);
     return n;
@@ -118,14 +174,14 @@ __device__ __forceinline__ int new_tokens(const RotatedParams &p, int b, int &L0
 constexpr int kBatch = 4;      // rows of every lane group under way
 
 // Q role.  Task = (token, span of p.q_span head batches).
-template <typename T, int D, bool INTER>
+template <typename T, int D, bool INTER, bool GIVEN>
 __device__ __forceinline__ void rotate_q(const RotatedParams &p, int b, int block) {
     constexpr int EPC = chunk16<T>::n, LPR = D / (2 * EPC), RPP = 32 / LPR;
     const int lane = threadIdx.x & 31, task = block * kWarps + (threadIdx.x >> 5);
     const int batches = (p.Hq + RPP * kBatch - 1) / (RPP * kBatch), spans = (batches + p.q_span - 1) / p.q_span;
     const int tok = task / spans, first = task % spans * p.q_span;
     if (tok >= p.T) return;
-    const LanePair l = lane_pair<EPC, INTER>(lane % LPR, p.rot);
+    LanePair l = lane_pair<EPC, INTER>(lane % LPR, p.rot);
     const T *q = static_cast<const T *>(p.q) + (size_t)b * p.q_batch + (size_t)tok * p.q_token;
     T *out = static_cast<T *>(p.q_out) + ((size_t)b * p.T + tok) * p.Hq * D;
     uint4 a[kBatch], c[kBatch];
@@ -143,12 +199,27 @@ __device__ __forceinline__ void rotate_q(const RotatedParams &p, int b, int bloc
     // the rows do not wait for the counts
     const bool early = !p.append_lens || p.T <= 8;
     if (early) fetch(first);
+    Given at;
+    bool there = true;
+    if constexpr (GIVEN) {
+        l.axes = pair_axes<EPC>(p, l.angle);
+        if (early) there = given_positions(p, b, tok, at);
+    }
     int L0;
-    const int n = new_tokens(p, b, L0, block == 0 && threadIdx.x == 0);
+    const int n = new_tokens<GIVEN>(p, b, L0, block == 0 && threadIdx.x == 0);
     if (tok >= n) return;
     if (!early) fetch(first);
     Angles<EPC> t;
-    load_angles<EPC>(t, p, L0 + tok, l);
+    if constexpr (GIVEN) {
+        if (!early) there = given_positions(p, b, tok, at);
+        if (!there) {
+            if (lane == 0 && p.status) atomicOr(p.status, QASA_DEVERR_POSITION);
+            return;
+        }
+        load_angles<EPC>(t, p, at, l);
+    } else {
+        load_angles<EPC>(t, p, L0 + tok, l);
+    }
     const int last = min(first + p.q_span, batches);
     for (int batch = first; batch < last; ++batch) {
         if (batch > first) fetch(batch);
@@ -169,8 +240,9 @@ __device__ __forceinline__ void rotate_q(const RotatedParams &p, int b, int bloc
 // 0.  False where there is nothing to do.
 struct PageSpan { int t_lo, t_hi, L0, page0, logical; bool fresh; };
 
+template <bool GIVEN>
 __device__ __forceinline__ bool page_span(const RotatedParams &p, int b, int page, bool report, PageSpan &s) {
-    const int n = new_tokens(p, b, s.L0, report && page == 0);
+    const int n = new_tokens<GIVEN>(p, b, s.L0, report && page == 0);
     s.logical = s.L0 / p.P + page;
     s.page0 = s.logical * p.P;
     s.t_lo = max(s.L0, s.page0);
@@ -199,57 +271,16 @@ __device__ __forceinline__ bool kv_task(const RotatedParams &p, int block, int &
     return h < p.Hkv;
 }
 
-// Minima and maxima of the stored keys of a lane's chunk pair, in the pool's own
-// type (exact, and half the registers of fp32 for 16-bit pools; E4M3 codes go as
-// halves).  A number wins over a NaN, as in the other box code.
-template <typename T> struct Box {
-    static constexpr int N = 8;                  // words of a chunk pair
-    uint32_t lo[N], hi[N];
-    static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) {
-        uint32_t r;
-        if constexpr (sizeof(T) == 4) r = __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
-        else if constexpr (elem<T>::id == QASA_DTYPE_BF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-    static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
-        uint32_t r;
-        if constexpr (sizeof(T) == 4) r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-        else if constexpr (elem<T>::id == QASA_DTYPE_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-    __device__ __forceinline__ void clear() {
-        const uint32_t inf = sizeof(T) == 4 ? 0x7f800000u : elem<T>::id == QASA_DTYPE_BF16 ? 0x7f807f80u : 0x7c007c00u;
-        const uint32_t minus = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
-#pragma unroll
-        for (int i = 0; i < N; ++i) { lo[i] = inf; hi[i] = inf | minus; }
-    }
-    __device__ __forceinline__ void fold(const uint4 &a, const uint4 &b) {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < N; ++i) { lo[i] = least(lo[i], w[i]); hi[i] = most(hi[i], w[i]); }
-    }
-    template <int LPR> __device__ __forceinline__ void join() {      // the warp's lane groups
-#pragma unroll
-        for (int off = LPR; off < 32; off <<= 1)
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                lo[i] = least(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
-                hi[i] = most(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
-            }
-    }
-};
-
 // KV role, pools of the inputs' type.
-template <typename T, int D, bool INTER>
+template <typename T, int D, bool INTER, bool GIVEN>
 __device__ __forceinline__ void append_kv(const RotatedParams &p, int b, int page, int block) {
     constexpr int EPC = chunk16<T>::n, LPR = D / (2 * EPC), RPP = 32 / LPR;
     PageSpan s;
     int h, which;
-    if (!page_span(p, b, page, block == 0 && threadIdx.x == 0, s) || !kv_task(p, block, h, which)) return;
+    if (!page_span<GIVEN>(p, b, page, block == 0 && threadIdx.x == 0, s) || !kv_task(p, block, h, which)) return;
     const int lane = threadIdx.x & 31, mine = s.t_lo + lane / LPR;
-    const LanePair l = lane_pair<EPC, INTER>(lane % LPR, p.rot);
+    LanePair l = lane_pair<EPC, INTER>(lane % LPR, p.rot);
+    if constexpr (GIVEN) l.axes = pair_axes<EPC>(p, l.angle);
     const T *src = (which ? static_cast<const T *>(p.v_new) + (size_t)b * p.v_batch
                           : static_cast<const T *>(p.k_new) + (size_t)b * p.k_batch) + (size_t)h * D;
     const long long stride = which ? p.v_token : p.k_token;
@@ -271,15 +302,25 @@ __device__ __forceinline__ void append_kv(const RotatedParams &p, int b, int pag
     T *dst = static_cast<T *>(which ? p.v_pool : p.k_pool) + ((size_t)phys * p.Hkv + h) * p.P * D;
     Box<T> box;
     box.clear();
+    bool any = !GIVEN;                           // a row has been stored
     for (int t0 = mine; t0 < s.t_hi; t0 += RPP * kBatch) {
         if (t0 > mine) fetch(t0);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int t = t0 + u * RPP;
             if (t >= s.t_hi) continue;
+            Given at;
+            if constexpr (GIVEN) {
+                if (!given_positions(p, b, t - s.L0, at)) {
+                    if (!which && h == 0 && p.status) atomicOr(p.status, QASA_DEVERR_POSITION);
+                    continue;
+                }
+                any = true;
+            }
             if (!which) {
                 Angles<EPC> ang;
-                load_angles<EPC>(ang, p, t, l);
+                if constexpr (GIVEN) load_angles<EPC>(ang, p, at, l);
+                else load_angles<EPC>(ang, p, t, l);
                 float y[2 * EPC];
                 rotate<T, INTER>(a[u], c[u], ang, l, y, y + EPC);
                 a[u] = chunk16<T>::pack(y);
@@ -292,6 +333,7 @@ __device__ __forceinline__ void append_kv(const RotatedParams &p, int b, int pag
         }
     }
     if (which) return;
+    if (GIVEN && !__any_sync(0xffffffffu, any)) return;
     box.template join<LPR>();
     if (lane < LPR) {
         T *row = static_cast<T *>(p.bounds) + ((size_t)phys * p.Hkv + h) * 2 * D;
@@ -308,81 +350,19 @@ __device__ __forceinline__ void append_kv(const RotatedParams &p, int b, int pag
     }
 }
 
-// Eight floats from eight codes.
-__device__ __forceinline__ void codes_to_f(const uint2 &w, float *f) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e4m3_to_f(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xffu);
-}
-// Two codes (low byte first), ties to even, saturating.
-__device__ __forceinline__ uint32_t code2(float lo, float hi) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
-    return c;
-}
-// Codes of y / s, the quotient rounded to fp32 as everywhere, eight at a time.
-__device__ __noinline__ uint2 quantise8_exact(float4 a, float4 b, float s) {
-    const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t w[2] = {0u, 0u};
-    if (s > 0.f)
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) w[e >> 2] |= code2(__fdiv_rn(y[e], s), __fdiv_rn(y[e + 1], s)) << (8 * (e & 2));
-    return make_uint2(w[0], w[1]);
-}
-// The division is needed only where a code border lies near: the product with the
-// reciprocal `inv` is within 2^-22 of the quotient (half a step each for the
-// reciprocal, the product and the quotient), so where products scaled by 1 - 2^-21
-// and 1 + 2^-21 have the same code, the quotient has it too.  The exact way is out
-// of line: the kernel's rows run into the instruction cache's size otherwise.
-__device__ __forceinline__ uint2 quantise8(const float *y, float s, float inv) {
-    uint32_t w[2] = {0u, 0u};
-    bool same = inv < INFINITY;                // a scale of 0, or one whose reciprocal is too large
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const float a = y[e] * inv, b = y[e + 1] * inv;
-        const uint32_t in = code2(a * (1.f - 0x1p-21f), b * (1.f - 0x1p-21f));
-        const uint32_t out = code2(a * (1.f + 0x1p-21f), b * (1.f + 0x1p-21f));
-        same = same && in == out;
-        w[e >> 2] |= out << (8 * (e & 2));
-    }
-    if (!same) {
-        const uint2 x = quantise8_exact(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), s);
-        w[0] = x.x;
-        w[1] = x.y;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) w[k] &= ((w[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | 0x7f7f7f7fu;   // zero is +0
-    return make_uint2(w[0], w[1]);
-}
-
-// Eight codes as halves, exactly, and back (halves that are codes' values).
-__device__ __forceinline__ uint4 codes_to_halves(const uint2 &w) {
-    return make_uint4(e4m3x2_to_h2(w.x), e4m3x2_to_h2(w.x >> 16), e4m3x2_to_h2(w.y), e4m3x2_to_h2(w.y >> 16));
-}
-__device__ __forceinline__ uint2 halves_to_codes(const uint32_t *h) {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint16_t c;
-        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h[i]));
-        w[i >> 1] |= (uint32_t)c << (16 * (i & 1));
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) w[k] &= ((w[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | 0x7f7f7f7fu;   // zero is +0
-    return make_uint2(w[0], w[1]);
-}
-
 // KV role, E4M3 pools: the page's scale follows the largest |value|, so the new
 // rows are gone through twice (largest value, then codes); where they fit they stay
 // in registers in between.  Where the scale grows the codes already in the page are
 // re-quantised, all in the fp32 steps that qasa_kv_append takes.
-template <int D, bool INTER>
+template <int D, bool INTER, bool GIVEN>
 __device__ __forceinline__ void append_kv_fp8(const RotatedParams &p, int b, int page, int block) {
     constexpr int EPC = 8, LPR = D / (2 * EPC), RPP = 32 / LPR;
     PageSpan s;
     int h, which;
-    if (!page_span(p, b, page, block == 0 && threadIdx.x == 0, s) || !kv_task(p, block, h, which)) return;
+    if (!page_span<GIVEN>(p, b, page, block == 0 && threadIdx.x == 0, s) || !kv_task(p, block, h, which)) return;
     const int lane = threadIdx.x & 31, mine = s.t_lo + lane / LPR;
     LanePair l = lane_pair<EPC, INTER>(lane % LPR, p.rot);
+    if constexpr (GIVEN) l.axes = pair_axes<EPC>(p, l.angle);
     if (which) l.turns = false;                  // V goes in as it is, through the same chunks
     const __half *src = (which ? static_cast<const __half *>(p.v_new) + (size_t)b * p.v_batch
                                : static_cast<const __half *>(p.k_new) + (size_t)b * p.k_batch) + (size_t)h * D;
@@ -399,10 +379,18 @@ __device__ __forceinline__ void append_kv_fp8(const RotatedParams &p, int b, int
             }
         }
     };
+    // false: the table has not the token's positions
     auto values = [&](int u, int t, float *y) {
         Angles<EPC> ang;
-        load_angles<EPC>(ang, p, t, l);
+        if constexpr (GIVEN) {
+            Given at;
+            if (!given_positions(p, b, t - s.L0, at)) return false;
+            load_angles<EPC>(ang, p, at, l);
+        } else {
+            load_angles<EPC>(ang, p, t, l);
+        }
         rotate<__half, INTER>(a[u], c[u], ang, l, y, y + EPC);
+        return true;
     };
     fetch(mine);
     const int phys = physical_page(p, b, s, block == 0 && threadIdx.x == 0);
@@ -411,19 +399,25 @@ __device__ __forceinline__ void append_kv_fp8(const RotatedParams &p, int b, int
     float *sc = p.scales + ((size_t)phys * p.Hkv + h) * 4 + which;
     const float old = s.fresh ? 0.f : *sc;
     float mx = 0.f;
+    bool any = false;                            // a row will be stored
     for (int t0 = mine; t0 < s.t_hi; t0 += RPP * kBatch) {
         if (t0 > mine) fetch(t0);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
             if (t0 + u * RPP < s.t_hi) {
                 float y[2 * EPC];
-                values(u, t0 + u * RPP, y);
+                if (!values(u, t0 + u * RPP, y)) {
+                    if (!which && h == 0 && p.status) atomicOr(p.status, QASA_DEVERR_POSITION);
+                    continue;
+                }
+                any = true;
 #pragma unroll
                 for (int e = 0; e < 2 * EPC; ++e) mx = fmaxf(mx, fabsf(y[e]));
             }
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (GIVEN && !__any_sync(0xffffffffu, any)) return;
     const float amax = fmaxf(old, mx);
     const float s_old = fp8_scale(old), s_new = fp8_scale(amax), inv = 1.f / s_new;
     const bool requant = !s.fresh && amax > old;
@@ -453,7 +447,7 @@ __device__ __forceinline__ void append_kv_fp8(const RotatedParams &p, int b, int
             if (t >= s.t_hi) continue;
             uint8_t *row = pool + (size_t)(t - s.page0) * D;
             float y[2 * EPC];
-            values(u, t, y);
+            if (!values(u, t, y)) continue;
             const uint2 qa = quantise8(y, s_new, inv), qb = quantise8(y + EPC, s_new, inv);
             *reinterpret_cast<uint2 *>(row + l.ca) = qa;
             *reinterpret_cast<uint2 *>(row + l.cb) = qb;
@@ -481,15 +475,15 @@ __device__ __forceinline__ void append_kv_fp8(const RotatedParams &p, int b, int
 }
 
 // T: the type of q and of the new rows; FP8: E4M3 pools.
-template <typename T, int D, bool FP8, bool INTER>
+template <typename T, int D, bool FP8, bool INTER, bool GIVEN>
 __global__ void __launch_bounds__(32 * kWarps, 5) append_rotated_kernel(RotatedParams p) {
     const int b = blockIdx.y, x = blockIdx.x;
     if (x < p.kv_blocks) {
         const int per_page = (2 * p.Hkv + kWarps - 1) / kWarps;
-        if constexpr (FP8) append_kv_fp8<D, INTER>(p, b, x / per_page, x % per_page);
-        else append_kv<T, D, INTER>(p, b, x / per_page, x % per_page);
+        if constexpr (FP8) append_kv_fp8<D, INTER, GIVEN>(p, b, x / per_page, x % per_page);
+        else append_kv<T, D, INTER, GIVEN>(p, b, x / per_page, x % per_page);
     } else {
-        rotate_q<T, D, INTER>(p, b, x - p.kv_blocks);
+        rotate_q<T, D, INTER, GIVEN>(p, b, x - p.kv_blocks);
     }
 }
 
@@ -511,7 +505,8 @@ cudaError_t launch_t(RotatedParams p, int batch, cudaStream_t stream) {
     const long long q = p.q ? ((batches + p.q_span - 1) / p.q_span * p.T + kWarps - 1) / kWarps : 0;
     if (kv + q > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     p.kv_blocks = (int)kv;
-    (p.interleaved ? append_rotated_kernel<T, D, FP8, true> : append_rotated_kernel<T, D, FP8, false>)
+    (p.positions ? p.interleaved ? append_rotated_kernel<T, D, FP8, true, true> : append_rotated_kernel<T, D, FP8, false, true>
+                 : p.interleaved ? append_rotated_kernel<T, D, FP8, true, false> : append_rotated_kernel<T, D, FP8, false, false>)
         <<<dim3((unsigned)(kv + q), batch), 32 * kWarps, 0, stream>>>(p);
     return cudaGetLastError();
 }

@@ -43,6 +43,11 @@ struct RotatedParams {
     int kv_blocks;       // blocks in x of the KV role, the rest rotate q
     int q_span;          // batches of query heads that a warp rotates
     int sms;             // SMs of the device
+    // positions given by the caller (NULL: those of the slots)
+    const int32_t *positions;
+    long long pos_axis, pos_batch;   // strides in elements
+    int num_axes;
+    uint32_t pair_axes[4];           // axis of each channel pair, two bits each
 };
 
 struct WindowParams {
@@ -66,6 +71,51 @@ struct WindowParams {
     int ws_pages;        // E4M3, prompt kernel: pages per sequence in the workspace
     unsigned long long wait_limit_ns;    // prompt kernel: waits on other warps
     unsigned long long drain_limit_ns;   // waits for the CTA's own copies and products (never shortened)
+    // trees of drafted tokens: [batch][T][mask_words], bit j of row t: query t sees the drafted token j
+    const int32_t *mask;
+    long long mask_batch;                // words from one sequence's mask to the next (0: all share one)
+    int mask_words;
+};
+
+struct KeepParams {
+    void *k_pool;
+    void *v_pool;
+    void *bounds;
+    float *scales;       // FP8 KV: [num_phys][Hkv][4] (amax K, amax V, -, -)
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    const int32_t *starts;
+    const int32_t *keep; // [batch][M]
+    const int32_t *keep_lens;
+    int32_t *lens_out;
+    int32_t *status;
+    int num_phys, Hkv, P, max_pages, M;
+    int cluster;         // CTAs that share a sequence's K or V of a KV head
+};
+
+struct PageCopyParams {
+    void *k_pool;
+    void *v_pool;
+    void *bounds;
+    float *scales;       // FP8 KV, else NULL
+    int32_t *status;
+    int num_phys, Hkv, P, row_chunks;    // 16-byte chunks of a row
+    int pieces;          // blocks per page
+    // copies
+    const int32_t *src_pages, *dst_pages;
+    // forks
+    const int32_t *block_table, *seq_lens, *parents, *new_pages;
+    int32_t *table_out, *lens_out;
+    int max_pages, batch;
+};
+
+struct TreeMaskParams {
+    const int32_t *parents;
+    const int32_t *lens;
+    int32_t *mask;
+    int32_t *depths;
+    int32_t *status;
+    int T, words;
 };
 
 struct SelectParams {
@@ -150,6 +200,13 @@ cudaError_t launch_append_rotated(qasa_dtype dt, int D, const RotatedParams &p, 
 // per (sequence, KV head) that it makes of `rows` rows.
 int window_row_tiles(qasa_dtype dt, int rows);
 cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
+// Trees of drafted tokens (p.mask).
+cudaError_t launch_tree_masks(const TreeMaskParams &p, int batch, cudaStream_t stream);
+cudaError_t launch_tree_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
+cudaError_t launch_keep(qasa_dtype dt, int D, const KeepParams &p, int batch, cudaStream_t stream);
+int page_pieces(const PageCopyParams &p);
+cudaError_t launch_copy_pages(const PageCopyParams &p, int pairs, cudaStream_t stream);
+cudaError_t launch_fork(const PageCopyParams &p, int children, cudaStream_t stream);
 // The same for many: 16-bit and E4M3 caches.  q: [batch * tokens][heads][d] in boxes of
 // 64 channels, G heads and 128 / G tokens; k, v: pool rows (E4M3: the rows that
 // launch_unpack_codes has written) in boxes of 64 channels and a page's rows; 128-byte

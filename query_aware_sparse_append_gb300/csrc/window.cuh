@@ -53,6 +53,25 @@ __device__ __forceinline__ bool sees(int i, int j, int window, int sinks) {
     return j <= i && (j < sinks || j > i - window);
 }
 
+// ------------------------------------------------------------------ trees
+// Queries t < n are drafted tokens at positions ctx + t, whose keys and values are in
+// the cache; among them query t sees what its mask row says.  It stands depth(t) tokens
+// behind the context, which decides what its window still has of that: the drafted
+// tokens that it sees, itself among them, minus one.
+__device__ __forceinline__ const uint32_t *tree_row(const WindowParams &p, int b, int t) {
+    return reinterpret_cast<const uint32_t *>(p.mask) + (size_t)b * p.mask_batch + (size_t)t * p.mask_words;
+}
+__device__ __forceinline__ int tree_depth(const WindowParams &p, const uint32_t *row, int n) {
+    int seen = 0;
+    for (int w = 0; 32 * w < n; ++w) seen += __popc(__ldg(row + w) & (n - 32 * w < 32 ? (1u << (n - 32 * w)) - 1u : ~0u));
+    return seen > 0 ? seen - 1 : 0;
+}
+// Whether the query of mask row `row` at position `pos` sees token j; tokens from ctx on are drafted ones.
+__device__ __forceinline__ bool tree_sees(const uint32_t *row, int pos, int j, int ctx, int len, int window, int sinks) {
+    if (j < ctx) return j < sinks || j > pos - window;
+    return j < len && (__ldg(row + ((j - ctx) >> 5)) >> ((j - ctx) & 31) & 1u);
+}
+
 // Weights are exp2(score - m) with m this far below the largest score (log2 units),
 // which the sums and outputs carry too, so that it cancels.  fp16 weights of the
 // largest scores are then 2^7, and only those 2^-21 times as large fall below its

@@ -29,6 +29,8 @@
 // same channels of two neighbouring rows and interleaves the halves with byte
 // permutes.  As in the prompt kernel a step's maximum is sought only where its
 // weights grow large.
+//
+// TREE: the queries are a tree of drafted tokens; only which tokens they see differs.
 #include "window.cuh"
 
 namespace qasa {
@@ -144,7 +146,7 @@ constexpr size_t step_smem() {
 }
 
 // T: type of q and out; FP8: pages of E4M3 codes (T is __half).
-template <typename T, bool FP8, int D, int ROWS, int W>
+template <typename T, bool FP8, int D, int ROWS, int W, bool TREE>
 __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(WindowParams p) {
     using R = Step<FP8, D>;
     constexpr int NH = ROWS / 8;              // query rows are the products' columns, 8 at a time
@@ -165,7 +167,9 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
     const int rows = min(ROWS, s.n * p.G - row0);
     if (rows <= 0) return;                    // the same for the whole cluster
     const int t0 = row0 / p.G, t1 = (row0 + rows - 1) / p.G;
-    const VisibleTiles vis = visible_tiles(s.first + t0, s.first + t1, p.window, p.sinks);
+    // a tree's queries may be at any depth and see any drafted token
+    const VisibleTiles vis = TREE ? visible_tiles(s.first, s.len - 1, p.window, p.sinks)
+                                  : visible_tiles(s.first + t0, s.first + t1, p.window, p.sinks);
     const int32_t *table = p.block_table + (size_t)b * p.max_pages;
 
     // This warp's tiles are number wg, wg + stride, ... of the visible ones.  Lane x
@@ -241,10 +245,15 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
     }
     // a lane's scores and outputs belong to query rows 8 x + 2 q4 and the one after
     int pos[NH][2];
+    const uint32_t *mask[NH][2];
 #pragma unroll
     for (int x = 0; x < NH; ++x)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) pos[x][e] = s.first + (row0 + min(8 * x + 2 * q4 + e, rows - 1)) / p.G;
+        for (int e = 0; e < 2; ++e) {
+            const int t = (row0 + min(8 * x + 2 * q4 + e, rows - 1)) / p.G;
+            if constexpr (TREE) mask[x][e] = tree_row(p, b, t);
+            pos[x][e] = s.first + (TREE ? tree_depth(p, mask[x][e], s.n) : t);
+        }
 
     // o[c][u]: channels 2 u (elements 0, 1) and 2 u + 1 (2, 3) of this lane's chunk c
     float o[R::VC][VCH / 2][NH][4];
@@ -285,8 +294,8 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
             const int x = i * TPS + t;
             tok0[t] = vis.tile(wg + x * stride) * kTile;
             good[t] = __shfl_sync(0xffffffffu, here.row, x - from) >= 0 && x < mine;
-            inside = inside && good[t] && tok0[t] + kTile - 1 <= s.first + t0 &&
-                     (tok0[t] + kTile <= p.sinks || tok0[t] > s.first + t1 - p.window);
+            inside = inside && good[t] && tok0[t] + kTile - 1 <= (TREE ? s.first - 1 : s.first + t0) &&
+                     (tok0[t] + kTile <= p.sinks || tok0[t] > (TREE ? s.len - 1 : s.first + t1) - p.window);
         }
 
         // scores: tokens g4 (elements 0, 1) and g4 + 8 (2, 3) of a tile
@@ -346,8 +355,12 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
                 for (int x = 0; x < NH; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!good[t] || !sees(pos[x][e & 1], tok0[t] + 8 * (e >> 1) + g4, p.window, p.sinks))
-                            sc[t][x][e] = -INFINITY;
+                    {
+                        const int j = tok0[t] + 8 * (e >> 1) + g4;
+                        const bool seen = TREE ? tree_sees(mask[x][e & 1], pos[x][e & 1], j, s.first, s.len, p.window, p.sinks)
+                                               : sees(pos[x][e & 1], j, p.window, p.sinks);
+                        if (!good[t] || !seen) sc[t][x][e] = -INFINITY;
+                    }
         }
         if constexpr (FP8) {
             float top = 0.f;
@@ -367,6 +380,7 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
             for (int t = 0; t < TPS; ++t) vs[t] *= inv_vref;
         }
         uint32_t pb[TPS][NH][2];
+        bool hidden[TPS][4];
         bool raise = unset;
         while (true) {
             if (raise) {                      // the step's own maximum
@@ -432,6 +446,17 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
         at = ring + slot * R::BYTES + 2 * q4 * ROWB;
 #pragma unroll
         for (int t = 0; t < TPS; ++t) {
+            if constexpr (TREE) {             // drafted tokens that none of these rows sees
+                if (!inside) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int j = tok0[t] + 2 * q4 + (y & 1) + 8 * (y >> 1) - s.first;
+                        bool any = j < 0 || j >= s.n;
+                        for (int i = t0; i <= t1 && !any; ++i) any = __ldg(tree_row(p, b, i) + (j >> 5)) >> (j & 31) & 1u;
+                        hidden[t][y] = !any;
+                    }
+                }
+            }
             uint4 vr[4][R::VC];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -448,7 +473,8 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
                     }
                     if (!inside) {            // values that no row sees may be anything: 0 * NaN is not 0
                         const int j = tok0[t] + r;
-                        if (!good[t] || j > vis.hi || (j < vis.lo && j >= p.sinks)) vr[y][c] = make_uint4(0, 0, 0, 0);
+                        if (!good[t] || j > vis.hi || (j < vis.lo && j >= p.sinks) || (TREE && hidden[t][y]))
+                            vr[y][c] = make_uint4(0, 0, 0, 0);
                     }
                 }
             }
@@ -513,7 +539,7 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
 // the ROWS scores of a row are summed over the four by a butterfly that leaves
 // each lane ROWS / 4 of them (all of them for ROWS < 4); the values are read a
 // whole row at a time, a lane owning D / 32 channels.
-template <int D, int ROWS, int W>
+template <int D, int ROWS, int W, bool TREE>
 __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p) {
     constexpr int KC = D / 16;                 // float4 chunks of a key row per lane
     constexpr int VN = D / 32;                 // channels per lane
@@ -533,8 +559,11 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
     const int rows = min(ROWS, s.n * p.G - row0);
     if (rows <= 0) return;
     const int t0 = row0 / p.G, t1 = (row0 + rows - 1) / p.G;
-    const VisibleTiles vis = visible_tiles(s.first + t0, s.first + t1, p.window, p.sinks);
+    const VisibleTiles vis = TREE ? visible_tiles(s.first, s.len - 1, p.window, p.sinks)
+                                  : visible_tiles(s.first + t0, s.first + t1, p.window, p.sinks);
     const int32_t *table = p.block_table + (size_t)b * p.max_pages;
+    __shared__ int depth[ROWS];               // TREE: depths of the rows
+    if (TREE && threadIdx.x < rows) depth[threadIdx.x] = tree_depth(p, tree_row(p, b, (row0 + threadIdx.x) / p.G), s.n);
 
     for (int x = threadIdx.x; x < ROWS * D / 4; x += W * 32) {
         const int r = x / (D / 4), c = x % (D / 4);
@@ -576,7 +605,12 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
             for (int t = 0; t < 8; ++t) {
                 const float *vrow = vpool + (size_t)(row + 8 * part + t) * D + lane * VN;
                 const int j = tile * kTile + 8 * part + t;
-                const bool any = j <= vis.hi && (j >= vis.lo || j < p.sinks);   // seen by some row
+                bool any = j <= vis.hi && (j >= vis.lo || j < p.sinks);         // seen by some row
+                if (TREE && any && j >= s.first) {
+                    any = false;
+                    for (int i = t0; i <= t1; ++i)
+                        any = any || (__ldg(tree_row(p, b, i) + ((j - s.first) >> 5)) >> ((j - s.first) & 31) & 1u);
+                }
                 if constexpr (VN == 4) {
                     const float4 x = __ldg(reinterpret_cast<const float4 *>(vrow));
                     vv[slot][t][0] = any ? x.x : 0.f; vv[slot][t][1] = any ? x.y : 0.f;
@@ -605,7 +639,10 @@ __global__ void __launch_bounds__(W * 32) window_rows_f32_kernel(WindowParams p)
                 a += __shfl_xor_sync(0xffffffffu, a, 1);
                 a += __shfl_xor_sync(0xffffffffu, a, 2);
                 const int t = (row0 + min(r, rows - 1)) / p.G;
-                sc[r] = sees(s.first + t, tok0 + g4, p.window, p.sinks) ? a * p.scale_log2 : -INFINITY;
+                const bool seen = TREE ? tree_sees(tree_row(p, b, t), s.first + depth[min(r, rows - 1)], tok0 + g4, s.first,
+                                                   s.len, p.window, p.sinks)
+                                       : sees(s.first + t, tok0 + g4, p.window, p.sinks);
+                sc[r] = seen ? a * p.scale_log2 : -INFINITY;
             }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
@@ -667,27 +704,27 @@ cudaError_t launch_rows(K kernel, const WindowParams &p, long long units, int th
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <typename T, bool FP8, int D>
+template <typename T, bool FP8, int D, bool TREE>
 cudaError_t launch_16(WindowParams p, cudaStream_t stream) {
     const int rows = p.T * p.G;
     if (rows <= 8) {
         p.row_tiles = 1;
-        return launch_rows(window_rows_kernel<T, FP8, D, 8, 4>, p, (long long)p.B * p.Hkv, 128, step_smem<FP8, D, 8, 4>(), stream);
+        return launch_rows(window_rows_kernel<T, FP8, D, 8, 4, TREE>, p, (long long)p.B * p.Hkv, 128, step_smem<FP8, D, 8, 4>(), stream);
     }
     p.row_tiles = (rows + 15) / 16;
-    return launch_rows(window_rows_kernel<T, FP8, D, 16, 4>, p, (long long)p.B * p.Hkv * p.row_tiles, 128,
+    return launch_rows(window_rows_kernel<T, FP8, D, 16, 4, TREE>, p, (long long)p.B * p.Hkv * p.row_tiles, 128,
                        step_smem<FP8, D, 16, 4>(), stream);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_f32(WindowParams p, cudaStream_t stream) {
     const int rows = p.T * p.G;
     if (rows == 1) {
         p.row_tiles = 1;
-        return launch_rows(window_rows_f32_kernel<D, 1, 4>, p, (long long)p.B * p.Hkv, 128, rows_smem<D, 1, 4>(), stream);
+        return launch_rows(window_rows_f32_kernel<D, 1, 4, TREE>, p, (long long)p.B * p.Hkv, 128, rows_smem<D, 1, 4>(), stream);
     }
     p.row_tiles = (rows + 7) / 8;
-    return launch_rows(window_rows_f32_kernel<D, 8, 4>, p, (long long)p.B * p.Hkv * p.row_tiles, 128,
+    return launch_rows(window_rows_f32_kernel<D, 8, 4, TREE>, p, (long long)p.B * p.Hkv * p.row_tiles, 128,
                        rows_smem<D, 8, 4>(), stream);
 }
 
@@ -699,15 +736,28 @@ int window_row_tiles(qasa_dtype dt, int rows) {
     return (rows + per - 1) / per;
 }
 
-cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream) {
+namespace {
+
+template <bool TREE>
+cudaError_t launch_any(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream) {
     switch (dt) {
-    case QASA_DTYPE_F32: return D == 64 ? launch_f32<64>(p, stream) : launch_f32<128>(p, stream);
+    case QASA_DTYPE_F32: return D == 64 ? launch_f32<64, TREE>(p, stream) : launch_f32<128, TREE>(p, stream);
     case QASA_DTYPE_F16:
-        return D == 64 ? launch_16<__half, false, 64>(p, stream) : launch_16<__half, false, 128>(p, stream);
+        return D == 64 ? launch_16<__half, false, 64, TREE>(p, stream) : launch_16<__half, false, 128, TREE>(p, stream);
     case QASA_DTYPE_BF16:
-        return D == 64 ? launch_16<__nv_bfloat16, false, 64>(p, stream) : launch_16<__nv_bfloat16, false, 128>(p, stream);
-    default: return D == 64 ? launch_16<__half, true, 64>(p, stream) : launch_16<__half, true, 128>(p, stream);
+        return D == 64 ? launch_16<__nv_bfloat16, false, 64, TREE>(p, stream)
+                       : launch_16<__nv_bfloat16, false, 128, TREE>(p, stream);
+    default: return D == 64 ? launch_16<__half, true, 64, TREE>(p, stream) : launch_16<__half, true, 128, TREE>(p, stream);
     }
+}
+
+}  // namespace
+
+cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream) {
+    return launch_any<false>(dt, D, p, stream);
+}
+cudaError_t launch_tree_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream) {
+    return launch_any<true>(dt, D, p, stream);
 }
 
 }  // namespace qasa
