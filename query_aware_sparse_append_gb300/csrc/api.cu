@@ -551,6 +551,30 @@ qasa_status append_rotated(const qasa_kv_cache *cache, const qasa_rotation *rota
     return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
 }
 
+// How a tree call runs: on the few-rows kernel, or on `ctas` CTAs that take units of
+// one or two row tiles of 128 rows, whole or cut where a CTA's share ends.
+struct TreePlan {
+    bool few, wide, whole;
+    int ctas;
+    TreeWorkspace ws;
+};
+
+TreePlan tree_plan(const qasa_kv_cache *c, int batch, int num_q_heads, int T, int max_pages) {
+    TreePlan r = {};
+    const int G = num_q_heads / c->num_kv_heads, per = 128 / G;
+    r.few = c->dtype == QASA_DTYPE_F32 || T * G <= 16;
+    if (r.few) return r;
+    r.wide = T > per;
+    const long long sms = sm_count() > 0 ? sm_count() : 152;
+    const long long units = (long long)batch * c->num_kv_heads * ((T + per * (r.wide ? 2 : 1) - 1) / (per * (r.wide ? 2 : 1)));
+    const long long tiles = ((long long)max_pages * c->page_size + 127) / 128;       // of a unit, at the most
+    r.whole = tiles <= 4;
+    const long long want = r.whole ? units : (units * (tiles + 2) + 3) / 4;
+    r.ctas = (int)(want < sms ? want : sms);
+    if (!r.whole) r.ws = tree_workspace(c->head_dim, r.wide, r.ctas);
+    return r;
+}
+
 // Whether the two stretches of memory have a byte in common (NULL: none).
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -825,8 +849,11 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
 
 size_t qasa_tree_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_kv_cache *cache,
                                 int32_t max_q_tokens, int32_t max_pages_per_seq) {
-    (void)batch; (void)num_q_heads; (void)cache; (void)max_q_tokens; (void)max_pages_per_seq;
-    return 0;
+    if (check_cache(cache) != QASA_OK || batch < 1 || batch > kMaxBatch || max_q_tokens < 1 || max_q_tokens > kMaxTreeTokens ||
+        max_pages_per_seq < 1 || max_pages_per_seq > kMaxPagesPerSeq || num_q_heads < cache->num_kv_heads ||
+        num_q_heads % cache->num_kv_heads || num_q_heads / cache->num_kv_heads > 8)
+        return 0;
+    return tree_plan(cache, batch, num_q_heads, max_q_tokens, max_pages_per_seq).ws.bytes;
 }
 
 qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,
@@ -848,8 +875,10 @@ qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32
     const void *ints[] = {q_lens, mask, device_status};
     for (const void *w : ints)
         if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
-    (void)workspace; (void)workspace_bytes;
-    WindowParams p = {};
+    const TreePlan plan = tree_plan(cache, batch, num_q_heads, max_q_tokens, max_pages_per_seq);
+    if (plan.ws.bytes && (!workspace || workspace_bytes < plan.ws.bytes || !aligned16(workspace))) return QASA_ERR_WORKSPACE;
+    TreeParams tp = {};
+    WindowParams &p = tp.w;
     p.q = q;
     p.out = out;
     p.k_pool = cache->k_pool;
@@ -874,6 +903,28 @@ qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32
     p.mask = mask;
     p.mask_batch = batch > 1 ? mask_batch_stride : 0;
     p.mask_words = words;
+    p.wait_limit_ns = wait_limit_ns();
+    p.drain_limit_ns = kWaitLimitNs;
+    if (!plan.few) {
+        CUtensorMap qm, km, vm;
+        st = query_tensor_map(&qm, q, cache->dtype, cache->head_dim, num_q_heads, p.G, (long long)batch * p.T);
+        if (st != QASA_OK) return st;
+        km = vm = qm;                             // E4M3 pages are copied untiled
+        if (cache->dtype != QASA_DTYPE_E4M3) {
+            st = pool_tensor_map(&km, cache->k_pool, cache, false);
+            if (st == QASA_OK) st = pool_tensor_map(&vm, cache->v_pool, cache, false);
+            if (st != QASA_OK) return st;
+        }
+        tp.whole_units = plan.whole;
+        if (plan.ws.bytes) {
+            unsigned char *at = static_cast<unsigned char *>(workspace);
+            tp.cuts = reinterpret_cast<int4 *>(at);
+            tp.part_ml = reinterpret_cast<float2 *>(at + plan.ws.ml);
+            tp.part_o = reinterpret_cast<float4 *>(at + plan.ws.o);
+        }
+        const cudaError_t e = launch_tree(cache->dtype, cache->head_dim, plan.wide, qm, km, vm, tp, plan.ctas, stream);
+        return e == cudaSuccess ? QASA_OK : QASA_ERR_CUDA;
+    }
     const long long tiles = most_visible_tiles(max_pages_per_seq, p.P, p.T, window, sink_tokens);
     const long long units = (long long)batch * p.Hkv * window_row_tiles(cache->dtype, p.T * p.G);
     p.cluster = window_cluster(cache->dtype, p.T * p.G, units, tiles);

@@ -77,6 +77,16 @@ struct WindowParams {
     int mask_words;
 };
 
+struct TreeParams {
+    WindowParams w;
+    int whole_units;     // a CTA takes whole units: nothing to join
+    int4 *cuts;          // [ctas] the unit whose first piece the CTA has (sequence, KV head, token; x < 0: none), last CTA
+    float2 *part_ml;     // [2 ctas][rows] maximum (log2 units) and sum of weights
+    float4 *part_o;      // [2 ctas][d / 4][rows]
+};
+// Byte offsets in a workspace (cuts lie first), and its size.
+struct TreeWorkspace { size_t ml, o, bytes; };
+
 struct KeepParams {
     void *k_pool;
     void *v_pool;
@@ -202,6 +212,11 @@ int window_row_tiles(qasa_dtype dt, int rows);
 cudaError_t launch_window_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
 // Trees of drafted tokens (p.mask).
 cudaError_t launch_tree_masks(const TreeMaskParams &p, int batch, cudaStream_t stream);
+// 16-bit and E4M3 caches, many rows: q, k, v as for launch_window_prompt (k, v not read for E4M3 pages).
+// wide: units of two row tiles.  ctas: at most one per SM.
+TreeWorkspace tree_workspace(int D, bool wide, int ctas);
+cudaError_t launch_tree(qasa_dtype dt, int D, bool wide, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                        const TreeParams &p, int ctas, cudaStream_t stream);
 cudaError_t launch_tree_rows(qasa_dtype dt, int D, const WindowParams &p, cudaStream_t stream);
 cudaError_t launch_keep(qasa_dtype dt, int D, const KeepParams &p, int batch, cudaStream_t stream);
 int page_pieces(const PageCopyParams &p);
