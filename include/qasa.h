@@ -454,7 +454,9 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
  *   workspace      device memory of qasa_tree_workspace_size bytes, 16-byte aligned
  *                  (scratch, no initialisation; NULL where that is 0).  Memory for a larger
  *                  batch, max_q_tokens and max_pages_per_seq serves every smaller call.
- * max_q_tokens up to 1024, any group size 1..8.  Precision, scale, bad pages, NaN
+ * max_q_tokens up to 1024, any group size 1..8; batch times num_kv_heads times the 128-token
+ * tiles of max_pages_per_seq pages (two more counted) times the blocks of 128 (256) query
+ * rows of a KV head up to 2^31 - 1.  Precision, scale, bad pages, NaN
  * queries and QASA_DEVERR_TIMEOUT as in qasa_window_attention; a query that sees
  * nothing gets zeros.  Keys and values must be finite of the context's tokens that a
  * query at depth 0 sees and of the drafted tokens that some query sees; other slots

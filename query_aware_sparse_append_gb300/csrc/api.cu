@@ -556,6 +556,7 @@ qasa_status append_rotated(const qasa_kv_cache *cache, const qasa_rotation *rota
 struct TreePlan {
     bool few, wide, whole;
     int ctas;
+    long long places;     // key tiles of all units, with two more for each
     TreeWorkspace ws;
 };
 
@@ -569,7 +570,8 @@ TreePlan tree_plan(const qasa_kv_cache *c, int batch, int num_q_heads, int T, in
     const long long units = (long long)batch * c->num_kv_heads * ((T + per * (r.wide ? 2 : 1) - 1) / (per * (r.wide ? 2 : 1)));
     const long long tiles = ((long long)max_pages * c->page_size + 127) / 128;       // of a unit, at the most
     r.whole = tiles <= 4;
-    const long long want = r.whole ? units : (units * (tiles + 2) + 3) / 4;
+    r.places = units * (tiles + 2);
+    const long long want = r.whole ? units : (r.places + 3) / 4;
     r.ctas = (int)(want < sms ? want : sms);
     if (!r.whole) r.ws = tree_workspace(c->head_dim, r.wide, r.ctas);
     return r;
@@ -876,6 +878,7 @@ qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32
     for (const void *w : ints)
         if (reinterpret_cast<uintptr_t>(w) & 3u) return QASA_ERR_ALIGN;
     const TreePlan plan = tree_plan(cache, batch, num_q_heads, max_q_tokens, max_pages_per_seq);
+    if (plan.places > 0x7fffffffLL) return QASA_ERR_SHAPE;
     if (plan.ws.bytes && (!workspace || workspace_bytes < plan.ws.bytes || !aligned16(workspace))) return QASA_ERR_WORKSPACE;
     TreeParams tp = {};
     WindowParams &p = tp.w;

@@ -91,6 +91,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
                  : "memory");
 }
 
+// Waits for the loads of 32 registers, whose uses cannot move before it.
+#define QASA_INOUT(x) "+r"(x)
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : QASA_R8(QASA_INOUT, 0), QASA_R8(QASA_INOUT, 8), QASA_R8(QASA_INOUT, 16), QASA_R8(QASA_INOUT, 24)
+                 :: "memory");
+}
+#undef QASA_INOUT
+
 #undef QASA_R8
 #undef QASA_OUT
 #undef QASA_IN

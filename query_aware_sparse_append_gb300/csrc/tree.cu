@@ -31,8 +31,9 @@
 // arrive under the last ones of the unit before.
 //
 // E4M3 pages come as codes and become halves, which they are exactly, on the way into the
-// ring.  The keys' scale multiplies the scores, the values' the weights: as a share of
-// the largest value scale so far, under which the output is kept.
+// ring.  The keys' scale multiplies the scores.  The values' scale, as a share of the largest one so far, under
+// which the output is kept, goes into the weights' exponents; the sum of a page's weights
+// is freed of it afterwards.
 #include "tcgen05.cuh"
 #include "window.cuh"
 
@@ -45,14 +46,15 @@ constexpr int kKeys = 128;            // tokens of a key tile
 constexpr int kUnitCost = 2;          // tiles that a unit's beginning and end are worth
 constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
 constexpr int kSegments = 4;          // segments told ahead
+constexpr float kLeastShare = -60.f;  // log2 of the least share of the largest value scale that a weight carries
 constexpr float kGivenUp = 3e38f;     // maximum that a CTA reports for rows that it gave up
-constexpr int kJoinThreads = 128, kJoinBlocks = 32;
+constexpr int kJoinThreads = 128, kJoinBatch = 4;
 
 template <bool FP8> constexpr int tree_threads() { return FP8 ? 512 : 384; }
 template <int D> constexpr int kv_bytes() { return kKeys * D * 2; }
 // Key and value tiles as halves, and as codes, under way.  128 channels: what fits.
-template <int D, bool FP8, bool WIDE> constexpr int kStages = D == 64 ? 8 : FP8 ? (WIDE ? 3 : 4) : 5;
-template <int D, bool FP8, bool WIDE> constexpr int kCodeStages = !FP8 ? 0 : D == 64 ? 6 : WIDE ? 4 : 3;
+template <int D, bool FP8, bool WIDE> constexpr int kStages = D == 64 ? 8 : FP8 ? 4 : 5;
+template <int D, bool FP8, bool WIDE> constexpr int kCodeStages = !FP8 ? 0 : D == 64 ? 6 : WIDE ? 2 : 3;
 template <int D, bool FP8, bool WIDE> constexpr size_t tree_smem() {
     return 1024 + (size_t)(WIDE ? 2 : 1) * kRows * D * 2 + (size_t)kStages<D, FP8, WIDE> * kv_bytes<D>() +
            (size_t)kCodeStages<D, FP8, WIDE> * kKeys * D + (WIDE ? 0 : 2 * 2 * kRows * sizeof(float2));
@@ -64,13 +66,16 @@ struct Pages {
     __device__ __forceinline__ int page(int k) const { return k < head ? k : body0 + k - head; }
 };
 
+__device__ __forceinline__ int page_shift(const WindowParams &p) { return p.P == 32 ? 5 : 4; }
+
 __device__ __forceinline__ Pages visible_pages(const WindowParams &p, const QuerySpan &s) {
     Pages v;
     v.hi = s.len - 1;
     v.lo = s.first - p.window + 1 > 0 ? s.first - p.window + 1 : 0;    // of a query at depth 0
-    v.body0 = v.lo / p.P;
-    v.head = min((min(p.sinks, v.lo) + p.P - 1) / p.P, v.body0);
-    v.count = s.len <= 0 ? 0 : v.head + v.hi / p.P - v.body0 + 1;
+    const int shift = page_shift(p);
+    v.body0 = v.lo >> shift;
+    v.head = min((min(p.sinks, v.lo) + p.P - 1) >> shift, v.body0);
+    v.count = s.len <= 0 ? 0 : v.head + (v.hi >> shift) - v.body0 + 1;
     return v;
 }
 
@@ -94,20 +99,34 @@ struct TreeShared {
     int failed;          // a bounded wait gave up: the rows that waited are not written
     int armed[8];        // copies into each stage (E4M3: of codes) so far
     int q_armed;
-    int seq0;            // the stretch begins in this sequence,
-    long long at0;       // whose first unit lies here on the line
-    long long total;
-    long long sums[16];
-    float ks[kScaleRing][kKeys / 16], vamax[kScaleRing][kKeys / 16];
+    int seq0, at0;       // the stretch begins in this sequence, whose first unit lies here on the line
+    QuerySpan span0;
+    int total, sums[16];
+    float ks[kScaleRing][kKeys / 16], lv[kScaleRing][kKeys / 16];   // E4M3: factor of the scores, log2 of the values' amax
     float unit[2][2];    // E4M3: unit of each group's output
 };
 
-// CTAs that share a line of `total` places (none of their stretches is empty), and where
-// the stretch of CTA c begins.
-__device__ __forceinline__ int sharers(long long total) { return total < gridDim.x ? (int)total : (int)gridDim.x; }
-__device__ __forceinline__ long long stretch(long long total, int c) {
-    const int C = sharers(total);
-    return c < C ? total * c / C : total;
+// How a line of `total` places (below 2^31) is shared: the first `more` CTAs have each + 1
+// places, the others `each`; with fewer places than CTAs the last ones have none.
+struct Line {
+    int each, more;
+    __device__ __forceinline__ explicit Line(int total) {
+        each = (int)((uint32_t)total / gridDim.x);
+        more = total - each * (int)gridDim.x;
+    }
+    __device__ __forceinline__ int begin(int c) const { return each * c + min(c, more); }
+    // the last CTA whose stretch begins before place `end` > 0
+    __device__ __forceinline__ int last_before(int end) const {
+        const int border = more * (each + 1);
+        return end <= border ? (int)((uint32_t)(end - 1) / (uint32_t)(each + 1))
+                             : more + (int)((uint32_t)(end - 1 - border) / (uint32_t)each);
+    }
+};
+
+// Units of a KV head of a sequence with n queries, tok_per of them to a unit; inv = 1 / tok_per,
+// exact enough for up to 1024 tokens.
+__device__ __forceinline__ int unit_blocks(int n, int tok_per, float inv) {
+    return __float2int_rd(((float)(n + tok_per - 1) + 0.5f) * inv);
 }
 
 // Walks the units that a CTA's stretch [v0, v1) of the line touches.  Of the unit at u0
@@ -115,46 +134,49 @@ __device__ __forceinline__ long long stretch(long long total, int c) {
 // beginning; `p.whole_units`: it has the whole unit if it begins in the stretch.
 struct Walk {
     const TreeParams &p;
-    long long v0, v1, u0, total;
-    int b, unit, units, tok_per;
+    const Line line;
+    int v0, v1, u0;
+    int b, unit, blocks, units, tok_per;
+    float inv_tok;
     QuerySpan s;
     Pages pages;
     int tiles;
-    __device__ __forceinline__ Walk(const TreeParams &p, int first, long long at, long long total, int tok_per)
-        : p(p), v0(stretch(total, blockIdx.x)), v1(stretch(total, blockIdx.x + 1)), u0(at), total(total),
-          b(first), unit(0), units(0), tok_per(tok_per) {
+    // the stretch begins in sequence `first`, of span `s`, whose first unit is at place `at`
+    __device__ __forceinline__ Walk(const TreeParams &p, int first, const QuerySpan &s, int at, int total, int tok_per, float inv_tok)
+        : p(p), line(total), v0(line.begin(blockIdx.x)), v1(line.begin(blockIdx.x + 1)), u0(at), b(first), unit(0), blocks(0),
+          units(0), tok_per(tok_per), inv_tok(inv_tok), s(s) {
         if (b < p.w.B) sequence();
     }
     __device__ __forceinline__ void sequence() {
-        s = query_span(p.w, b, false);
         pages = visible_pages(p.w, s);
         tiles = (pages.count * p.w.P + kKeys - 1) / kKeys;
-        units = p.w.Hkv * ((s.n + tok_per - 1) / tok_per);
+        blocks = unit_blocks(s.n, tok_per, inv_tok);
+        units = p.w.Hkv * blocks;
         unit = 0;
         // units that end before the stretch
         if (units > 0 && v0 > u0) {
-            const long long skip = (v0 - u0) / (tiles + kUnitCost);
-            unit = (int)(skip < units ? skip : units);
-            u0 += (long long)unit * (tiles + kUnitCost);
+            unit = min((int)((uint32_t)(v0 - u0) / (uint32_t)(tiles + kUnitCost)), units);
+            u0 += unit * (tiles + kUnitCost);
         }
     }
     __device__ __forceinline__ bool next(Segment &g) {
         while (b < p.w.B && u0 < v1) {
             if (unit == units) {
-                if (++b < p.w.B) sequence();
+                if (++b < p.w.B) {
+                    s = query_span(p.w, b, false);
+                    sequence();
+                }
                 continue;
             }
-            const int blocks = units / p.w.Hkv;
-            const long long lo = v0 - u0 - kUnitCost, hi = v1 - u0 - kUnitCost;
-            g.t0 = v0 <= u0 || lo < 0 ? 0 : (int)lo;
-            g.t1 = hi < tiles ? (int)(hi > 0 ? hi : 0) : tiles;
+            g.t0 = v0 <= u0 ? 0 : max(v0 - u0 - kUnitCost, 0);
+            g.t1 = min(max(v1 - u0 - kUnitCost, 0), tiles);
             if (p.whole_units) {
                 g.t0 = 0;
                 g.t1 = u0 >= v0 ? tiles : 0;
             }
             g.b = b;
-            g.h = unit / blocks;
-            g.tok0 = unit % blocks * tok_per;
+            g.h = blocks == 1 ? unit : (int)((uint32_t)unit / (uint32_t)blocks);
+            g.tok0 = (unit - g.h * blocks) * tok_per;
             g.tiles = tiles;
             g.s = s;
             g.pages = pages;
@@ -163,15 +185,15 @@ struct Walk {
             ++unit;
             if (!take) continue;
             // the last stretch that begins before the unit's end
-            g.last_cta = (int)((u0 * sharers(total) - 1) / total);
+            g.last_cta = line.last_before(u0);
             // full tiles of context pages wholly inside the deepest row's window
-            const int ppt = kKeys / p.w.P, ctx = s.first;
+            const int shift = page_shift(p.w), ppt = kKeys >> shift, ctx = s.first;
             g.whole0 = g.whole1 = 0;
             if (ctx > 0) {
-                const int clear = max(s.len - 1 - p.w.window + p.w.P, 0) / p.w.P;
-                g.whole0 = (pages.head + max(clear - pages.body0, 0) + ppt - 1) / ppt;
-                if (pages.head > 0) g.whole0 = max(g.whole0, (pages.head + ppt - 1) / ppt);
-                g.whole1 = (pages.head + max(ctx / p.w.P - pages.body0, 0)) / ppt;
+                const int clear = max(s.len - 1 - p.w.window + p.w.P, 0) >> shift;
+                g.whole0 = (pages.head + max(clear - pages.body0, 0) + ppt - 1) >> (7 - shift);
+                if (pages.head > 0) g.whole0 = max(g.whole0, (pages.head + ppt - 1) >> (7 - shift));
+                g.whole1 = (pages.head + max((ctx >> shift) - pages.body0, 0)) >> (7 - shift);
             }
             return true;
         }
@@ -189,12 +211,67 @@ __device__ __forceinline__ uint32_t upto16(int x, int base) {
     const int n = x - base;
     return n < 0 ? 0u : n >= 15 ? 0xffffu : (2u << n) - 1u;
 }
-// Bits `at` .. at + 15 of a mask row of `words` words (at > -16; those that it has not are 0).
-__device__ __forceinline__ uint32_t mask16(const uint32_t *row, int words, int at) {
-    if (at < 0) return __ldg(row) << -at & 0xffffu;
-    const int w = at >> 5;
-    const uint32_t lo = w < words ? __ldg(row + w) : 0u, hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+// The words of mask rows that hold the drafted tokens of a key tile: first word, and the
+// first token's number among the drafted ones.
+constexpr int kMaskWords = 5;
+__device__ __forceinline__ int tile_word(const WindowParams &p, const Segment &g, int tile) {
+    const int k = tile * (kKeys >> page_shift(p));
+    const int at = k < g.pages.head ? 0 : (g.pages.page(k) << page_shift(p)) - g.s.first;
+    return max(at, 0) >> 5;
+}
+__device__ __forceinline__ void load_words(const WindowParams &p, const uint32_t *row, int word, uint32_t *w) {
+#pragma unroll
+    for (int i = 0; i < kMaskWords; ++i) w[i] = word + i < p.mask_words ? __ldg(row + word + i) : 0u;
+}
+// Bits at .. at + 15 (at > -16) of words that begin with number `word`.
+__device__ __forceinline__ uint32_t bits16(const uint32_t *w, int word, int at) {
+    if (at < 0) return w[0] << -at & 0xffffu;
+    const int i = (at >> 5) - word;
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int x = 0; x < kMaskWords; ++x) {
+        if (x == i) lo = w[x];
+        if (x == i + 1) hi = w[x];
+    }
     return __funnelshift_r(lo, hi, at & 31) & 0xffffu;
+}
+
+// Which tokens of a key tile a query at `pos` with these mask words sees, all pages taken for good.
+struct Seen { uint32_t w[4]; };
+__device__ __forceinline__ Seen visible(const WindowParams &p, const Segment &g, int tile, int pos, const uint32_t *words,
+                                        int word) {
+    Seen r = {};
+    const int shift = page_shift(p), ctx = g.s.first;
+#pragma unroll 1
+    for (int q = 0; q < kKeys / 16; ++q) {
+        const int k = (tile << (7 - shift)) + (q >> (shift - 4));
+        if (k >= g.pages.count) break;
+        const int base = (g.pages.page(k) << shift) + (q * 16 & (p.P - 1));
+        uint32_t seen = upto16(ctx - 1, base) & (upto16(p.sinks - 1, base) | ~upto16(pos - p.window, base));
+        if (base + 15 >= ctx) seen |= bits16(words, word, base - ctx) & upto16(g.s.len - 1, base);
+        const uint32_t put = seen << (q & 1) * 16;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x == q >> 1) r.w[x] |= put;
+    }
+    return r;
+}
+// Only the tokens of good pages.
+__device__ __forceinline__ void only_good(const WindowParams &p, const Segment &g, int tile, Seen &r) {
+    const int shift = page_shift(p);
+#pragma unroll 1
+    for (int q = 0; q < kKeys / 16; ++q) {
+        const int k = (tile << (7 - shift)) + (q >> (shift - 4));
+        if (k < g.pages.count && good_page(p, p.block_table + (size_t)g.b * p.max_pages, g.pages.page(k))) continue;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x == q >> 1) r.w[x] &= ~(0xffffu << (q & 1) * 16);
+    }
+}
+
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (elem<T>::id == QASA_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
 // Two fp32 operations in one instruction; register pairs hold neighbouring columns.
@@ -217,21 +294,36 @@ __device__ __forceinline__ int slot_of(int cta, bool first) { return 2 * cta + (
 
 // Whether the tile may have value rows that no row of the unit sees.
 __device__ __forceinline__ bool hidden_rows(const WindowParams &p, TreeShared &sh, const Segment &g, int tile) {
-    const int ppt = kKeys / p.P, k0 = tile * ppt, k1 = k0 + ppt;
+    const int ppt = kKeys >> page_shift(p), k0 = tile * ppt, k1 = k0 + ppt;
     return *(volatile int *)&sh.any_bad != 0 || k1 >= g.pages.count || g.pages.page(k1 - 1) * p.P + p.P > g.s.first ||
            (g.pages.lo > 0 && k0 <= g.pages.head && k1 >= g.pages.head);
 }
-// Whether some row of the unit may see row r of the tile.
-__device__ __forceinline__ bool row_seen(const WindowParams &p, TreeShared &sh, const Segment &g, int tile, int r, int tok_per) {
-    const int k = tile * (kKeys / p.P) + r / p.P, pg = g.pages.page(k), at = pg * p.P + r % p.P;
-    if (k >= g.pages.count || at > g.pages.hi || (at < g.pages.lo && at >= p.sinks)) return false;
-    if (*(volatile int *)&sh.any_bad && !good_page(p, p.block_table + (size_t)g.b * p.max_pages, pg)) return false;
-    const int j = at - g.s.first;
-    if (j < 0) return true;
+// Union of the mask words of the unit's tokens, for a whole warp.
+__device__ __forceinline__ void any_words(const WindowParams &p, const Segment &g, int tok_per, int word, uint32_t *any) {
     const int end = min(g.s.n, g.tok0 + tok_per);
-    for (int t = g.tok0; t < end; ++t)
-        if (__ldg(tree_row(p, g.b, t) + (j >> 5)) >> (j & 31) & 1u) return true;
-    return false;
+#pragma unroll
+    for (int i = 0; i < kMaskWords; ++i) any[i] = 0;
+    for (int t = g.tok0 + (threadIdx.x & 31); t < end; t += 32) {
+        uint32_t w[kMaskWords];
+        load_words(p, tree_row(p, g.b, t), word, w);
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i) any[i] |= w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kMaskWords; ++i) any[i] = __reduce_or_sync(0xffffffffu, any[i]);
+}
+// The rows of the tile that some row of the unit may see, for a whole warp.
+__device__ __forceinline__ Seen seen_rows(const WindowParams &p, TreeShared &sh, const Segment &g, int tile, int tok_per) {
+    const int word = tile_word(p, g, tile);
+    uint32_t any[kMaskWords];
+    any_words(p, g, tok_per, word, any);
+    Seen r = visible(p, g, tile, g.s.first, any, word);
+    if (*(volatile int *)&sh.any_bad) only_good(p, g, tile, r);
+    return r;
+}
+__device__ __forceinline__ bool row_seen(const Seen &s, int r) {
+    const uint32_t w = r < 64 ? (r < 32 ? s.w[0] : s.w[1]) : (r < 96 ? s.w[2] : s.w[3]);
+    return w >> (r & 31) & 1u;
 }
 
 // T: 16-bit type of q and out (and of the pages); FP8: pages of E4M3 codes.
@@ -290,40 +382,57 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         if (tp.cuts) tp.cuts[cta] = make_int4(-1, 0, 0, 0);
     }
     if (warp == MMA) tmem_alloc(&sh.tmem, TMEM);
+    if (warp == LOAD && lane == 0) {
+        prefetch_tensormap(&qmap);
+        if (!FP8) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
+    }
 
     // The length of the line, and the sequence in which this CTA's stretch begins: a
     // thread adds up a run of sequences, the warps' sums are added in order.
+    const float inv_tok = 1.f / tok_per;
     {
-        const int run = (p.B + THREADS - 1) / THREADS, b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
-        auto cost = [&](int b, bool report) {
-            const QuerySpan s = query_span(p, b, report);
+        const int run = p.B <= THREADS ? 1 : (p.B + THREADS - 1) / THREADS, b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
+        auto cost = [&](const QuerySpan &s) {
             const Pages v = visible_pages(p, s);
-            return (long long)p.Hkv * ((s.n + tok_per - 1) / tok_per) * ((v.count * p.P + kKeys - 1) / kKeys + kUnitCost);
+            return p.Hkv * unit_blocks(s.n, tok_per, inv_tok) * ((v.count * p.P + kKeys - 1) / kKeys + kUnitCost);
         };
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += cost(b, cta == 0);
-        long long before = mine;
+        int mine = 0, c = 0;
+        QuerySpan s{};
+        for (int b = b0; b < b1; ++b) {
+            s = query_span(p, b, cta == 0);
+            c = cost(s);
+            mine += c;
+        }
+        int before = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, before, o);
+            const int x = __shfl_up_sync(0xffffffffu, before, o);
             if (lane >= o) before += x;
         }
         if (lane == 31) sh.sums[warp] = before;
         before -= mine;
         __syncthreads();
-        long long total = 0;
+        int total = 0;
+#pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) {
             if (w == warp) before += total;
             total += sh.sums[w];
         }
         if (tid == 0) sh.total = total;
-        const long long v0 = stretch(total, cta);
+        const int v0 = Line(total).begin(cta);
         if (v0 >= before && v0 < before + mine)
-            for (int b = b0; b < b1; ++b) {
-                const long long c = cost(b, false);
+            for (int b = b0;; ++b) {
+                if (run > 1) {
+                    s = query_span(p, b, false);
+                    c = cost(s);
+                }
                 if (v0 < before + c) {
                     sh.seq0 = b;
                     sh.at0 = before;
+                    sh.span0 = s;
                     break;
                 }
                 before += c;
@@ -332,6 +441,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();              // the joining kernel takes the SMs that are done, and waits there for the others
     const uint32_t tmem = sh.tmem;
     auto give_up = [&] {
         *(volatile int *)&sh.failed = 1;
@@ -376,28 +486,35 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         uint32_t done = 0, tile_base = 0;                         // tiles of this group, of the CTA so far
         for (uint32_t seg = 0; begin(seg); ++seg) {
             const Segment &g = sh.seg[seg % kSegments];
-            const int n = g.t1 - g.t0, ppt = kKeys / p.P;
+            const int n = g.t1 - g.t0;
             const int tok = g.tok0 + (WIDE ? i * per : 0) + row / p.G, head = g.h * p.G + row % p.G;
             const bool live = row < per * p.G && tok < g.s.n;
             const bool busy = __any_sync(0xffffffffu, live);      // a warp without rows only keeps pace
-            const int32_t *table = p.block_table + (size_t)g.b * p.max_pages;
             const uint32_t *mask = tree_row(p, g.b, live ? tok : 0);
             const int pos = g.s.first + (live ? tree_depth(p, mask, g.s.n) : 0);
             const int mine = WIDE ? (i < row_tiles(g) ? n : 0) : (n + 1 - i) / 2;
             float m = live ? -INFINITY : 0.f, l = 0.f;
-            float vref = 0.f, inv_vref = 0.f;                     // E4M3: O is in units of the largest V amax so far
+            float lref = -INFINITY;                               // E4M3: O is in units of 2^lref, the largest V amax so far
             bool unset = true;                                    // a row of the warp has seen nothing yet
             for (int k = 0; ok && k < mine; ++k) {
                 const int j = WIDE ? k : 2 * k + i, tile = g.t0 + j;
+                bool masked = tile < g.whole0 || tile >= g.whole1;
+                Seen seen = {{~0u, ~0u, ~0u, ~0u}};
+                if (busy && masked) {                             // before the scores are there
+                    uint32_t words[kMaskWords];
+                    const int word = tile_word(p, g, tile);
+                    load_words(p, mask, word, words);
+                    seen = visible(p, g, tile, pos, words, word);
+                }
                 if (!wait(&sh.s_full[i], done & 1)) { ok = false; break; }
                 ++done;
                 tc_fence_after();
                 if (busy) {
                     const uint32_t scales_at = (tile_base + j) % kScaleRing;
-                    uint32_t x[kKeys];
-                    bool raise = unset, raised = false;
-                    const bool bad = *(volatile int *)&sh.any_bad != 0;
-                    const bool masked = bad || tile < g.whole0 || tile >= g.whole1;
+                    if (*(volatile int *)&sh.any_bad) {
+                        only_good(p, g, tile, seen);
+                        masked = true;
+                    }
                     auto scale_o = [&](float f) {                 // the last product into O is complete: S of this tile follows it
                         if (k == 0) return;
 #pragma unroll 1
@@ -412,85 +529,107 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                         tmem_wait_st();
                     };
                     if constexpr (FP8) {
-                        float top = 0.f;
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int q = 0; q < kKeys / 16; ++q) top = fmaxf(top, sh.vamax[scales_at][q]);
-                        if (top > vref) {
-                            scale_o(vref / top);
-                            vref = top;
-                            inv_vref = 1.f / top;
+                        for (int q = 0; q < kKeys / 16; ++q) top = fmaxf(top, sh.lv[scales_at][q]);
+                        if (top > lref) {
+                            scale_o(exp2_fast(lref - top));
+                            lref = top;
                         }
                     }
-                    while (true) {
+                    // 32 tokens at a time, in a loop: its instructions, which every SM fetches anew in
+                    // every launch, are a quarter of those of the whole tile
+                    auto load_chunk = [&](int c, uint32_t *x) {
+                        tmem_ld32(sa + 32 * c, x);
+                        const uint32_t w = c < 2 ? (c == 0 ? seen.w[0] : seen.w[1]) : (c == 2 ? seen.w[2] : seen.w[3]);
+                        tmem_wait_ld32(x);
+                        if (masked)
 #pragma unroll
-                        for (int c = 0; c < kKeys; c += 32) tmem_ld32(sa + c, x + c);
-                        tmem_wait_ld();
-                        if (masked) {
-                            const int ctx = g.s.first, last = g.s.len - 1;
+                            for (int e = 0; e < 32; ++e)
+                                if (!(w >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
+                    };
+                    auto scale_of = [&](int c, int h) { return FP8 ? sh.ks[scales_at][2 * c + h] : p.scale_log2; };
+                    auto largest = [&](int c, const uint32_t *x) {
+                        float top = -INFINITY;
 #pragma unroll
-                            for (int q = 0; q < kKeys / 16; ++q) {
-                                const int e = tile * ppt + q * 16 / p.P, pg = g.pages.page(e);
-                                const int base = pg * p.P + q * 16 % p.P;
-                                uint32_t seen = 0;
-                                if (e < g.pages.count && (!bad || good_page(p, table, pg))) {
-                                    seen = upto16(ctx - 1, base) & (upto16(p.sinks - 1, base) | ~upto16(pos - p.window, base));
-                                    if (base + 15 >= ctx)
-                                        seen |= mask16(mask, p.mask_words, base - ctx) & upto16(last, base);
-                                }
+                        for (int h = 0; h < 2; ++h) {
+                            float t[4];
 #pragma unroll
-                                for (int c = 0; c < 16; ++c)
-                                    if (!(seen >> c & 1u)) x[q * 16 + c] = __float_as_uint(-INFINITY);
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                t[e] = fmaxf(fmaxf(__uint_as_float(x[h * 16 + e]), __uint_as_float(x[h * 16 + 4 + e])),
+                                             fmaxf(__uint_as_float(x[h * 16 + 8 + e]), __uint_as_float(x[h * 16 + 12 + e])));
+                            top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_of(c, h));
                         }
-                        if (raise) {
-                            float top = -INFINITY;
+                        return top;
+                    };
+                    if (unset) {                                  // the tile's own maximum
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < kKeys / 32; ++c) {
+                            uint32_t x[32];
+                            load_chunk(c, x);
+                            top = fmaxf(top, largest(c, x));
+                        }
+                        const float m_new = fmaxf(m, top - kHeadroom<T>);
+                        const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
+                        m = m_new;
+                        l *= f;
+                        scale_o(f);
+                        unset = __any_sync(0xffffffffu, m == -INFINITY);
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        uint32_t x[32], w16[16];
+                        load_chunk(c, x);
+                        float add;
+                        for (bool again = false;; again = true) {
+                            const float base = m == -INFINITY ? 0.f : m;
+                            add = 0.f;
 #pragma unroll
-                            for (int q = 0; q < kKeys / 16; ++q) {
-                                float t[4];
+                            for (int h = 0; h < 2; ++h) {
+                                const float scale = scale_of(c, h);
+                                const float share = FP8 ? fmaxf(sh.lv[scales_at][2 * c + h] - lref, kLeastShare) : 0.f;
+                                float2 sum[2] = {};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    t[e] = fmaxf(fmaxf(__uint_as_float(x[q * 16 + e]), __uint_as_float(x[q * 16 + 4 + e])),
-                                                 fmaxf(__uint_as_float(x[q * 16 + 8 + e]), __uint_as_float(x[q * 16 + 12 + e])));
-                                top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (FP8 ? sh.ks[scales_at][q] : 1.f));
+                                for (int e = 0; e < 16; e += 2) {
+                                    float2 w = fma2(x[h * 16 + e], x[h * 16 + e + 1], scale, share - base);
+                                    w.x = exp2_fast(w.x);
+                                    w.y = exp2_fast(w.y);
+                                    sum[e / 2 & 1] = add2(sum[e / 2 & 1], w);
+                                    // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
+                                    w16[(h * 16 + e) / 2] = mma16816<T>::pack2(w.x, w.y);
+                                }
+                                sum[0] = add2(sum[0], sum[1]);
+                                const float s2 = sum[0].x + sum[0].y;
+                                add = FP8 ? fmaf(s2, exp2_fast(-share), add) : add + s2;
                             }
-                            const float m_new = fmaxf(m, top * p.scale_log2 - kHeadroom<T>);
-                            const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
-                            m = m_new;
+                            if (again || !__any_sync(0xffffffffu, live && !(add <= kMostWeight))) break;
+                            // Weights that grow large: the maximum rises by a whole number, so that what there
+                            // is of the tile's weights is scaled by a power of two, without another rounding.
+                            float rise = add <= kMostWeight ? 0.f : ceilf(largest(c, x) - kHeadroom<T> - m);
+                            rise = rise > 0.f ? rise : 0.f;
+                            const float f = rise < 127.f ? __int_as_float((127 - (int)rise) << 23) : 0.f;
+                            m += rise;
                             l *= f;
                             scale_o(f);
-                            unset = __any_sync(0xffffffffu, m == -INFINITY);
-                            raised = true;
-                        }
-                        const float base = m == -INFINITY ? 0.f : m;
-                        float2 sum[4] = {};
+                            tmem_wait_st();
+#pragma unroll 1
+                            for (int before = 0; before < c; ++before) {
+                                uint32_t y[16];
+                                tmem_ld16(sa + 16 * before, y);
+                                tmem_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < kKeys / 16; ++q) {
-                            float vs = 1.f, scale = p.scale_log2;
-                            if constexpr (FP8) {
-                                vs = sh.vamax[scales_at][q] * inv_vref;
-                                scale *= sh.ks[scales_at][q];
-                            }
-#pragma unroll
-                            for (int c = 0; c < 16; c += 2) {
-                                const int e = q * 16 + c;
-                                float2 w = fma2(x[e], x[e + 1], scale, -base);
-                                w.x = exp2_fast(w.x);
-                                w.y = exp2_fast(w.y);
-                                sum[c / 2 & 3] = add2(sum[c / 2 & 3], w);
-                                // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
-                                x[e / 2] = FP8 ? mma16816<T>::pack2(w.x * vs, w.y * vs) : mma16816<T>::pack2(w.x, w.y);
+                                for (int e = 0; e < 16; ++e) {
+                                    const float2 v = unpack2<T>(y[e]);
+                                    y[e] = mma16816<T>::pack2(v.x * f, v.y * f);
+                                }
+                                tmem_st16(sa + 16 * before, y);
                             }
                         }
-                        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-                        const float add = sum[0].x + sum[0].y;
-                        if (raised || !__any_sync(0xffffffffu, live && !(add <= kMostWeight))) {
-                            l += add;
-                            break;
-                        }
-                        raise = true;
+                        // over scores that have been read: columns 16 c .. of chunk c / 2
+                        tmem_st16(sa + 16 * c, w16);
+                        l += add;
                     }
-#pragma unroll
-                    for (int c = 0; c < kKeys / 2; c += 32) tmem_st32(sa + c, x + c);
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -507,7 +646,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
             // WIDE: a thread has its row to itself; else the two groups have a part of the
             // same row each, and a thread of either takes half of the channels.
             if (mine == 0) l = 0.f;
-            float f0 = FP8 ? fp8_scale(vref) : 1.f, f1 = 0.f;     // factors of this group's output and of the other's
+            float f0 = FP8 && mine > 0 ? fp8_scale(exp2_fast(lref)) : 1.f, f1 = 0.f;     // factors of this group's output and of the other's
             if constexpr (!WIDE) {
                 float2 *now = states + (seg & 1) * 2 * kRows;
                 now[i * kRows + row] = make_float2(m, l);
@@ -564,7 +703,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
             tc_fence_before();
             mbar_arrive(&sh.o_free);
             if (tid == 0 && g.t0 == 0 && !whole)
-                tp.cuts[cta] = make_int4(g.b, g.h, g.tok0, g.last_cta);
+                tp.cuts[cta] = make_int4(g.b, g.h, g.tok0 | min(g.s.n - g.tok0, tok_per) << 16, g.last_cta);
             end(seg);
         }
     } else if (warp == MMA) {
@@ -673,32 +812,30 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
         // lane brings the codes of a page, one contiguous stretch.
         constexpr int PER_PAGE = FP8 ? 1 : NB;
         constexpr int RS = FP8 ? NC : NS;                         // stages that copies go to
-        if (lane == 0) {
-            prefetch_tensormap(&qmap);
-            if (!FP8) {
-                prefetch_tensormap(&kmap);
-                prefetch_tensormap(&vmap);
-            }
-        }
         uint32_t item = 0, loaded = 0, tile_base = 0;
-        const int ppt = kKeys / p.P;
+        const int ppt = kKeys >> page_shift(p);
         for (uint32_t seg = 0; begin(seg); ++seg) {
             const Segment &g = sh.seg[seg % kSegments];
             const int n = g.t1 - g.t0;
             const int32_t *table = p.block_table + (size_t)g.b * p.max_pages;
-            float2 amax = make_float2(0.f, 0.f);                  // of the lane's page
-            auto look_up = [&](int j) {                           // its first pool row, or -1
-                const int k = (g.t0 + j) * ppt + lane / PER_PAGE;
-                if (lane >= ppt * PER_PAGE || j >= n || k >= g.pages.count) return -1;
+            // a lane holds the place of page number `from` + lane of the list, and of the one 32 further on
+            struct Place { int row; float2 amax; };               // first pool row, or -1
+            auto look_up = [&](int at) {
+                Place x{-1, make_float2(0.f, 0.f)};
+                const int k = at + lane;
+                if (k >= min(g.pages.count, g.t1 * ppt)) return x;
                 const int phys = table[g.pages.page(k)];
                 if (phys >= 0 && phys < p.num_phys) {
-                    if constexpr (FP8) amax = *reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + g.h) * 4);
-                    return (phys * p.Hkv + g.h) * p.P;
+                    x.row = (phys * p.Hkv + g.h) * p.P;
+                    if constexpr (FP8) x.amax = *reinterpret_cast<const float2 *>(p.scales + ((size_t)phys * p.Hkv + g.h) * 4);
+                } else {
+                    *(volatile int *)&sh.any_bad = 1;
+                    if (p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
                 }
-                *(volatile int *)&sh.any_bad = 1;
-                if (p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
-                return -1;
+                return x;
             };
+            int from = g.t0 * ppt;
+            Place here = look_up(from), there = look_up(from + 32);
             auto bring = [&](int v, int row) {                    // the keys or values of a tile
                 const uint32_t st = item % RS;
                 uint64_t *full = FP8 ? &sh.code_full[st] : &sh.kv_full[st], *empty = FP8 ? &sh.code_empty[st] : &sh.kv_empty[st];
@@ -720,37 +857,50 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                 }
                 ++item;
             };
-            int row = look_up(0), before = -1;                    // of this tile and of the one before
+            auto bring_queries = [&] {
+                ok = loaded == 0 || wait(&sh.q_empty, (loaded - 1) & 1);
+                if (ok && lane == 0) {
+                    const int q_tiles = row_tiles(g);
+                    sh.q_armed = loaded + 1;
+                    mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_tiles * NB * per * p.G * 128));
+                    for (int i = 0; i < q_tiles; ++i)
+                        for (int c = 0; c < NB; ++c)
+                            tma_load_3d(qtile + (i * NB + c) * BLOCK, &qmap, &sh.q_full, c * 64, g.h * p.G,
+                                        g.b * p.T + g.tok0 + i * per);
+                }
+                ++loaded;
+            };
+            // the first queries at once, later ones, which wait for the unit before, behind the first keys
+            const int queries_at = loaded == 0 ? -1 : (n < LEAD ? n : LEAD) - 1;
+            if (n > 0 && queries_at < 0) bring_queries();
+            int row = -1, before = -1;                            // the lane's page of this tile and of the one before
             for (int t = 0; ok && t < n + LEAD - 1; ++t) {
                 if (t < n) {
+                    const int at = (g.t0 + t) * ppt;
+                    if (at - from >= 32) {
+                        from += 32;
+                        here = there;
+                        there = look_up(from + 32);
+                    }
+                    row = __shfl_sync(0xffffffffu, here.row, (at - from + lane / PER_PAGE) & 31);
+                    if (lane >= ppt * PER_PAGE) row = -1;
                     if constexpr (FP8) {
+                        const float ka = __shfl_sync(0xffffffffu, here.amax.x, (at - from + lane) & 31);
+                        const float va = __shfl_sync(0xffffffffu, here.amax.y, (at - from + lane) & 31);
                         // a page without keys has the scale 0, under which a hidden score's -inf would be NaN
-                        const int at = (tile_base + t) % kScaleRing;
+                        const float ks = row >= 0 ? fmaxf(fp8_scale(ka), 1e-30f) * p.scale_log2 : 1.f;
+                        const float lv = row >= 0 && va > 0.f ? log2f(va) : -140.f;
                         for (int q = lane * p.P / 16; lane < ppt && q < (lane + 1) * p.P / 16; ++q) {
-                            sh.ks[at][q] = row >= 0 ? fmaxf(fp8_scale(amax.x), 1e-30f) : 1.f;
-                            sh.vamax[at][q] = row >= 0 ? amax.y : 0.f;
+                            sh.ks[(tile_base + t) % kScaleRing][q] = ks;
+                            sh.lv[(tile_base + t) % kScaleRing][q] = lv;
                         }
                         __syncwarp();
                     }
                     bring(0, row);
                 }
-                if (ok && t == (n < LEAD ? n : LEAD) - 1) {       // the queries, behind the first keys
-                    ok = loaded == 0 || wait(&sh.q_empty, (loaded - 1) & 1);
-                    if (ok && lane == 0) {
-                        const int q_tiles = row_tiles(g);
-                        sh.q_armed = loaded + 1;
-                        mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(q_tiles * NB * per * p.G * 128));
-                        for (int i = 0; i < q_tiles; ++i)
-                            for (int c = 0; c < NB; ++c)
-                                tma_load_3d(qtile + (i * NB + c) * BLOCK, &qmap, &sh.q_full, c * 64, g.h * p.G,
-                                            g.b * p.T + g.tok0 + i * per);
-                    }
-                    ++loaded;
-                }
-                const int next = look_up(t + 1);
+                if (ok && t == queries_at) bring_queries();
                 if (ok && t >= LEAD - 1) bring(1, LEAD == 1 ? row : before);
                 before = row;
-                row = next;
             }
             tile_base += n;
             end(seg);
@@ -771,8 +921,9 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                 if (!ok) break;
                 if constexpr (!FP8) {
                     if (hidden_rows(p, sh, g, g.t0 + j)) {
+                        const Seen seen = seen_rows(p, sh, g, g.t0 + j, tok_per);
                         for (int r = lane; r < kKeys; r += 32)
-                            if (!row_seen(p, sh, g, g.t0 + j, r, tok_per))
+                            if (!row_seen(seen, r))
 #pragma unroll
                                 for (int c = 0; c < NB * 8; ++c)
                                     *reinterpret_cast<uint4 *>(ring + st * kv_bytes<D>() + (c / 8) * BLOCK + r * 128 + c % 8 * 16) =
@@ -801,7 +952,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     } else if (warp == PLAN) {
         // ------------------------------------------------------------ segments
         if (lane == 0) {
-            Walk walk(tp, sh.seq0, sh.at0, sh.total, tok_per);
+            Walk walk(tp, sh.seq0, sh.span0, sh.at0, sh.total, tok_per, inv_tok);
             Segment next;
             for (uint32_t seg = 0;; ++seg) {
                 if (!walk.next(next)) next.b = -1;
@@ -819,7 +970,14 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     } else if (FP8 && warp >= CONVERT) {
         // ------------------------------------------------------ codes to halves
         constexpr int CPR = D / 16;                               // 16-code chunks of a row
-        const int me = tid - CONVERT * 32;
+        // A thread takes the same chunk of every eighth (or a multiple) row, so that its places in
+        // the swizzled tile are a stride apart.  The halves of a chunk's codes go to two places; the
+        // two 64-channel blocks lie in the same banks: half of the lanes store them the other way round.
+        const uint32_t me = tid - CONVERT * 32, c = me % CPR, r0 = me / CPR;
+        constexpr uint32_t ROW_STEP = 128 / CPR;
+        const bool swap = c / 4 & 1;
+        const uint32_t place = (2 * c / 8) * BLOCK + r0 * 128, chunk = (2 * c % 8 ^ (r0 & 7)) * 16;
+        const uint32_t first = place + (swap ? chunk ^ 16 : chunk), second = place + (swap ? chunk : chunk ^ 16);
         uint32_t item = 0;
         for (uint32_t seg = 0; begin(seg); ++seg) {
             const Segment &g = sh.seg[seg % kSegments];
@@ -833,21 +991,30 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                 ok = wait(&sh.code_full[cs], item / (NC ? NC : 1) & 1) && (item < NS || wait(&sh.kv_empty[st], (item / NS - 1) & 1));
                 if (!ok) break;
                 const bool clean = v && hidden_rows(p, sh, g, tile);
-                const unsigned char *from = codes + cs * kKeys * D;
+                Seen seen = {};
+                if (clean) seen = seen_rows(p, sh, g, tile, tok_per);
+                const unsigned char *from = codes + cs * kKeys * D + me * 16;
                 unsigned char *to = ring + st * kv_bytes<D>();
-#pragma unroll 4
-                for (int x = me; x < kKeys * CPR; x += 128) {
-                    const int r = x / CPR, c = x % CPR;
-                    uint4 w = *reinterpret_cast<const uint4 *>(from + x * 16), lo, hi;
-                    if (clean && !row_seen(p, sh, g, tile, r, tok_per)) w = make_uint4(0, 0, 0, 0);
-                    codes_to_h(w.x, &lo.x);
-                    codes_to_h(w.y, &lo.z);
-                    codes_to_h(w.z, &hi.x);
-                    codes_to_h(w.w, &hi.z);
-                    unsigned char *base = to + (2 * c / 8) * BLOCK + r * 128;
-                    const int a = 2 * c % 8 ^ (r & 7), odd = c / 4 & 1;      // the two blocks' chunks lie in the same banks
-                    *reinterpret_cast<uint4 *>(base + (odd ? a ^ 1 : a) * 16) = odd ? hi : lo;
-                    *reinterpret_cast<uint4 *>(base + (odd ? a : a ^ 1) * 16) = odd ? lo : hi;
+                constexpr int BATCH = 4, STEPS = kKeys * CPR / 128;
+#pragma unroll
+                for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
+                    uint4 w[BATCH];
+#pragma unroll
+                    for (int u = 0; u < BATCH; ++u) w[u] = *reinterpret_cast<const uint4 *>(from + (s0 + u) * 2048);
+                    if (clean)
+#pragma unroll
+                        for (int u = 0; u < BATCH; ++u)
+                            if (!row_seen(seen, r0 + (s0 + u) * ROW_STEP)) w[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < BATCH; ++u) {
+                        uint4 h;
+                        codes_to_h(swap ? w[u].z : w[u].x, &h.x);
+                        codes_to_h(swap ? w[u].w : w[u].y, &h.z);
+                        *reinterpret_cast<uint4 *>(to + first + (s0 + u) * ROW_STEP * 128) = h;
+                        codes_to_h(swap ? w[u].x : w[u].z, &h.x);
+                        codes_to_h(swap ? w[u].y : w[u].w, &h.z);
+                        *reinterpret_cast<uint4 *>(to + second + (s0 + u) * ROW_STEP * 128) = h;
+                    }
                 }
                 fence_async_smem();
                 mbar_arrive(&sh.code_empty[cs]);
@@ -878,47 +1045,62 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
 }
 
 // Joins the pieces of the units that borders of stretches cut: the unit whose first piece
-// CTA blockIdx.x has goes on in the CTAs after it, up to cuts[].w.  A thread takes eight
-// channels of a row, its pieces in the order of the CTAs.
+// CTA blockIdx.y has goes on in the CTAs after it, up to cuts[].w.  A thread takes eight
+// channels of a row and its pieces in the order of the CTAs, kJoinBatch of them under way at
+// once, states and outputs together: after the cut's record one round trip to L2 is all
+// that a unit of few pieces waits for.
 template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeParams tp) {
     constexpr int ROWS = (WIDE ? 2 : 1) * kRows;
-    pdl_wait();
-    const int cta = blockIdx.x;
-    const int4 cut = tp.cuts[cta];
-    if (cut.x < 0) return;
+    const int cta = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const WindowParams &p = tp.w;
-    const QuerySpan s = query_span(p, cut.x, false);
-    const int per = kRows / p.G, tile_rows = per * p.G, rows = min((s.n - cut.z) * p.G, (WIDE ? 2 : 1) * tile_rows);
-    for (int x = blockIdx.y * kJoinThreads + threadIdx.x; x < rows * (D / 8); x += kJoinBlocks * kJoinThreads) {
-        const int r = x % rows, c = x / rows;                     // neighbours have neighbouring rows
-        const int at = r / tile_rows * kRows + r % tile_rows;
-        float top = -INFINITY;
-        for (int k = cta; k <= cut.w; ++k) {
-            const float2 ml = tp.part_ml[(size_t)slot_of(k, k == cta) * ROWS + at];
-            if (ml.y != 0.f) top = fmaxf(top, ml.x);
-        }
-        float sum = 0.f, o[8] = {};
-#pragma unroll 4
-        for (int k = cta; k <= cut.w; ++k) {
-            const int slot = slot_of(k, k == cta);
-            const float2 ml = tp.part_ml[(size_t)slot * ROWS + at];
-            const float4 *part = tp.part_o + ((size_t)slot * (D / 4) + 2 * c) * ROWS + at;
-            const float4 a = part[0], b = part[ROWS];
-            const float f = ml.y != 0.f ? exp2_fast(ml.x - top) : 0.f;
-            if (ml.y == 0.f) continue;                            // NaN included: it goes through to the row
-            sum = fmaf(f, ml.y, sum);
-            o[0] = fmaf(f, a.x, o[0]); o[1] = fmaf(f, a.y, o[1]); o[2] = fmaf(f, a.z, o[2]); o[3] = fmaf(f, a.w, o[3]);
-            o[4] = fmaf(f, b.x, o[4]); o[5] = fmaf(f, b.y, o[5]); o[6] = fmaf(f, b.z, o[6]); o[7] = fmaf(f, b.w, o[7]);
-        }
-        if (sum < 0.f) continue;                                  // a CTA gave up: the row stays as it was
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;           // a row that sees nothing is zero
+    const int per = kRows / p.G, tile_rows = per * p.G;
+    const int r = (int)(blockIdx.x / (D / 32)) * 32 + lane, c = (int)(blockIdx.x % (D / 32)) * 4 + warp;   // row, eight channels
+    pdl_wait();
+    const int4 cut = tp.cuts[cta];
+    const int tok0 = cut.z & 0xffff, rows = (cut.z >> 16) * p.G;
+    if (cut.x < 0 || r >= rows) return;
+    const int at = r < tile_rows ? r : kRows + r - tile_rows;
+    float top = -INFINITY, sum = 0.f, o[8] = {};
+    for (int k0 = cta; k0 <= cut.w; k0 += kJoinBatch) {
+        float2 ml[kJoinBatch];
+        float4 a[kJoinBatch], b[kJoinBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= inv;
-        const int tok = cut.z + r / p.G;
-        T *dst = static_cast<T *>(p.out) + (((size_t)cut.x * p.T + tok) * p.Hq + cut.y * p.G + r % p.G) * D + 8 * c;
-        *reinterpret_cast<uint4 *>(dst) = chunk16<T>::pack(o);
+        for (int u = 0; u < kJoinBatch; ++u) {
+            const int k = k0 + u, slot = slot_of(k, k == cta);
+            ml[u] = make_float2(-INFINITY, 0.f);
+            a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k <= cut.w) {
+                const float4 *part = tp.part_o + ((size_t)slot * (D / 4) + 2 * c) * ROWS + at;
+                ml[u] = tp.part_ml[(size_t)slot * ROWS + at];
+                a[u] = part[0];
+                b[u] = part[ROWS];
+            }
+        }
+        float now = top;
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u)
+            if (ml[u].y != 0.f) now = fmaxf(now, ml[u].x);
+        const float old = now == top ? 1.f : exp2_fast(top - now);
+        top = now;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= old;
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u) {
+            if (ml[u].y == 0.f) continue;                         // its output was never written; NaN included goes through
+            const float f = exp2_fast(ml[u].x - top);
+            sum = fmaf(f, ml[u].y, sum);
+            o[0] = fmaf(f, a[u].x, o[0]); o[1] = fmaf(f, a[u].y, o[1]); o[2] = fmaf(f, a[u].z, o[2]); o[3] = fmaf(f, a[u].w, o[3]);
+            o[4] = fmaf(f, b[u].x, o[4]); o[5] = fmaf(f, b[u].y, o[5]); o[6] = fmaf(f, b[u].z, o[6]); o[7] = fmaf(f, b[u].w, o[7]);
+        }
     }
+    if (sum < 0.f) return;                                        // a CTA gave up: the row stays as it was
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;               // a row that sees nothing is zero
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= inv;
+    T *dst = static_cast<T *>(p.out) + (((size_t)cut.x * p.T + tok0 + r / p.G) * p.Hq + cut.y * p.G + r % p.G) * D + 8 * c;
+    *reinterpret_cast<uint4 *>(dst) = chunk16<T>::pack(o);
 }
 
 template <typename T, bool FP8, int D, bool WIDE>
@@ -939,7 +1121,7 @@ cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorM
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)ctas, kJoinBlocks);
+    cfg.gridDim = dim3((WIDE ? 2 : 1) * kRows / 32 * (D / 32), (unsigned)ctas);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.attrs = at;
