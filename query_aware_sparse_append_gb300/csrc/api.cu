@@ -560,21 +560,60 @@ struct TreePlan {
     TreeWorkspace ws;
 };
 
+// QASA_TREE_FORM (diagnostic, for tests of each form): "rows" the few-rows kernel, "whole"
+// and "cut" the tree kernel with whole and with cut units; NULL: by the rules below.
+const char *tree_form() {
+    const char *v = std::getenv("QASA_TREE_FORM");
+    return v && (v[0] == 'r' || v[0] == 'w' || v[0] == 'c') ? v : nullptr;
+}
+
+// The few-rows kernel goes through a unit's keys once for every 16 rows, the tree kernel
+// once for 128 or 256, but takes 5 to 8 us more to begin and to join.  Times in us of few |
+// tree, 16-bit, d = 128; A: 1 x 500 tokens of 8 KV heads, B: 1 x 4000, C: 16 x 500 of 4
+// heads, D: 16 x 4000, E: 64 x 1000 of 8, F: 64 x 8000 of 4; E4M3 in brackets:
+//   rows      16                     32                    64                  128
+//   A    9|14  (11|16)        10|14  (12|16)       11|19  (13|19)      21|20 (24|20)
+//   B   15|18  (16|19)        16|18  (16|19)       18|19  (19|20)      37|20 (40|21)
+//   C   20|15  (23|17)        14|15  (16|17)       17|15  (18|17)      32|20 (37|20)
+//   D   42|38  (39|40)        40|39  (38|40)       75|39  (71|41)     147|40 (140|41)
+//   E   64|67  (54|77)        76|67  (80|78)      136|71 (135|81)     262|86 (272|92)
+//   F  160|182 (136|212)     281|183 (263|212)    441|190 (410|218)   812|192 (738|219)
+// In key tiles of 128 tokens and 128 channels a row tile is worth 8 ns on the few-rows
+// kernel, a tile 10.5 (13) ns on the tree kernel.  The few-rows kernel's clusters of eight do
+// not fill the device with few units: 32000 tokens of 8 heads take 55 to 66 us for up to 16
+// rows there, 38 us here.
 TreePlan tree_plan(const qasa_kv_cache *c, int batch, int num_q_heads, int T, int max_pages) {
     TreePlan r = {};
     const int G = num_q_heads / c->num_kv_heads, per = 128 / G;
-    r.few = c->dtype == QASA_DTYPE_F32 || T * G <= 16;
+    const long long sms = sm_count() > 0 ? sm_count() : 152;
+    const long long pairs = (long long)batch * c->num_kv_heads, row_tiles = ((long long)T * G + 15) / 16;
+    const long long tiles = ((long long)max_pages * c->page_size + 127) / 128;       // of a unit, at the most
+    const bool eight = c->dtype == QASA_DTYPE_E4M3, fills = pairs * row_tiles * 8 >= sms || tiles <= 64;
+    const long long more = (10 * row_tiles - (eight ? 16 : 13)) * (pairs * tiles * c->head_dim / 128);
+    const char *form = tree_form();
+    r.few = c->dtype == QASA_DTYPE_F32 || (form ? form[0] == 'r' : fills && more <= (eight ? 8750 : 6400));
     if (r.few) return r;
     r.wide = T > per;
-    const long long sms = sm_count() > 0 ? sm_count() : 152;
-    const long long units = (long long)batch * c->num_kv_heads * ((T + per * (r.wide ? 2 : 1) - 1) / (per * (r.wide ? 2 : 1)));
-    const long long tiles = ((long long)max_pages * c->page_size + 127) / 128;       // of a unit, at the most
-    r.whole = tiles <= 4;
+    const long long units = pairs * ((T + per * (r.wide ? 2 : 1) - 1) / (per * (r.wide ? 2 : 1)));
+    // Whole units where they are short, or many and not long: 512 units of 9 tiles take the
+    // same time either way, or less whole (E4M3 102 and 76 us), 256 of 63 tiles 182 and 198.
+    r.whole = form ? form[0] == 'w' : tiles <= 4 || (tiles <= 16 && units >= 3 * sms);
     r.places = units * (tiles + 2);
     const long long want = r.whole ? units : (r.places + 3) / 4;
     r.ctas = (int)(want < sms ? want : sms);
     if (!r.whole) r.ws = tree_workspace(c->head_dim, r.wide, r.ctas);
     return r;
+}
+
+// Workspace that serves this call and every smaller one, which may run the other way.
+size_t tree_most_workspace(const qasa_kv_cache *c, int batch, int num_q_heads, int T, int max_pages) {
+    if (c->dtype == QASA_DTYPE_F32) return 0;
+    const int per = 128 / (num_q_heads / c->num_kv_heads);
+    const bool wide = T > per;
+    const long long sms = sm_count() > 0 ? sm_count() : 152;
+    const long long units = (long long)batch * c->num_kv_heads * ((T + per * (wide ? 2 : 1) - 1) / (per * (wide ? 2 : 1)));
+    const long long want = (units * (((long long)max_pages * c->page_size + 127) / 128 + 2) + 3) / 4;
+    return tree_workspace(c->head_dim, wide, (int)(want < sms ? want : sms)).bytes;
 }
 
 // Whether the two stretches of memory have a byte in common (NULL: none).
@@ -855,7 +894,7 @@ size_t qasa_tree_workspace_size(int32_t batch, int32_t num_q_heads, const qasa_k
         max_pages_per_seq < 1 || max_pages_per_seq > kMaxPagesPerSeq || num_q_heads < cache->num_kv_heads ||
         num_q_heads % cache->num_kv_heads || num_q_heads / cache->num_kv_heads > 8)
         return 0;
-    return tree_plan(cache, batch, num_q_heads, max_q_tokens, max_pages_per_seq).ws.bytes;
+    return tree_most_workspace(cache, batch, num_q_heads, max_q_tokens, max_pages_per_seq);
 }
 
 qasa_status qasa_tree_attention(const qasa_kv_cache *cache, const void *q, int32_t num_q_heads,

@@ -91,7 +91,7 @@ struct Segment {
 
 struct TreeShared {
     uint64_t q_full, q_empty, kv_full[8], kv_empty[8], code_full[6], code_empty[6];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free, joined, drained;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], joined, drained;
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     Segment seg[kSegments];
     uint32_t tmem;
@@ -373,7 +373,10 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
             mbar_init(&sh.seg_full[i], 1);
             mbar_init(&sh.seg_empty[i], FP8 ? 15 : 11);           // a warp each, but this one's
         }
-        mbar_init(&sh.o_free, 2 * kRows);
+        // An output may be written again when it has been read: WIDE by its own group, else (the
+        // first barrier alone) by both.  Segments in which it was not written do not count: a group
+        // that idles through some would otherwise arrive in the other's place.
+        for (int i = 0; i < NQ; ++i) mbar_init(&sh.o_free[i], WIDE ? kRows : 2 * kRows);
         mbar_init(&sh.joined, 2 * kRows);
         mbar_init(&sh.drained, 1);
         sh.any_bad = sh.failed = sh.q_armed = 0;
@@ -459,13 +462,13 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     auto row_tiles = [&](const Segment &g) { return NQ == 2 && g.tok0 + per < g.s.n ? 2 : 1; };
 
     // registers go to the softmax warps, within what the block was launched with:
-    // 256 x 208 + 128 x 88 = 384 x 168, 256 x 184 + 256 x 72 = 512 x 128
+    // 256 x 192 + 128 x 120 = 384 x 168, 256 x 160 + 256 x 96 = 512 x 128
     if (warp < MMA) {
-        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     } else {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     }
 
     bool ok = true;
@@ -491,7 +494,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
             const bool live = row < per * p.G && tok < g.s.n;
             const bool busy = __any_sync(0xffffffffu, live);      // a warp without rows only keeps pace
             const uint32_t *mask = tree_row(p, g.b, live ? tok : 0);
-            const int pos = g.s.first + (live ? tree_depth(p, mask, g.s.n) : 0);
+            int pos = -1;                                         // context and depth, once a tile needs it
             const int mine = WIDE ? (i < row_tiles(g) ? n : 0) : (n + 1 - i) / 2;
             float m = live ? -INFINITY : 0.f, l = 0.f;
             float lref = -INFINITY;                               // E4M3: O is in units of 2^lref, the largest V amax so far
@@ -504,6 +507,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                     uint32_t words[kMaskWords];
                     const int word = tile_word(p, g, tile);
                     load_words(p, mask, word, words);
+                    if (pos < 0) pos = max(g.s.first + (p.window < g.s.len ? tree_depth(p, mask, g.s.n) : 0), 0);
                     seen = visible(p, g, tile, pos, words, word);
                 }
                 if (!wait(&sh.s_full[i], done & 1)) { ok = false; break; }
@@ -677,31 +681,33 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                 T *dst = static_cast<T *>(p.out) + (((size_t)g.b * p.T + tok) * p.Hq + head) * D + c0;
                 float4 *part = tp.part_o + ((size_t)slot * (D / 4) + c0 / 4) * ROWS + (WIDE ? i * kRows : 0) + row;
 #pragma unroll 1
-                for (int c = 0; c < COLS; c += 16) {
-                    uint32_t o[16], u[16];
-                    if (mine > 0) tmem_ld16(oa + c0 + c, o);
-                    if (!WIDE && n > 1 - i) tmem_ld16(tmem + lanes + O_COL[1 - i] + c0 + c, u);
-                    tmem_wait_ld();
-                    float v[16];
+                for (int c = 0; c < COLS; c += 32) {
+                    uint32_t o[32], u[32];
+                    if (mine > 0) tmem_ld32(oa + c0 + c, o);
+                    if (!WIDE && n > 1 - i) tmem_ld32(tmem + lanes + O_COL[1 - i] + c0 + c, u);
+                    tmem_wait_ld32(o);
+                    if (!WIDE) tmem_wait_ld32(u);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {                // 0 of something that was never written is not 0
-                        v[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
-                        if (!WIDE) v[e] += f1 != 0.f ? __uint_as_float(u[e]) * f1 : 0.f;
-                    }
-                    if (whole) {
-                        if (live)
+                    for (int e8 = 0; e8 < 32; e8 += 8) {
+                        float v[8];
 #pragma unroll
-                            for (int e = 0; e < 16; e += 8) *reinterpret_cast<uint4 *>(dst + c + e) = chunk16<T>::pack(v + e);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            part[(size_t)(c + e) / 4 * ROWS] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        for (int e = 0; e < 8; ++e) {             // 0 of something that was never written is not 0
+                            v[e] = f0 != 0.f ? __uint_as_float(o[e8 + e]) * f0 : 0.f;
+                            if (!WIDE) v[e] += f1 != 0.f ? __uint_as_float(u[e8 + e]) * f1 : 0.f;
+                        }
+                        if (whole) {
+                            if (live) *reinterpret_cast<uint4 *>(dst + c + e8) = chunk16<T>::pack(v);
+                        } else {
+                            float4 *to = part + (size_t)(c + e8) / 4 * ROWS;
+                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            to[ROWS] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
                     }
                 }
                 if (!whole && (WIDE || i == 0)) tp.part_ml[(size_t)slot * ROWS + (WIDE ? i * kRows : 0) + row] = make_float2(m, l);
             }
             tc_fence_before();
-            mbar_arrive(&sh.o_free);
+            if (WIDE ? mine > 0 : n > 0) mbar_arrive(&sh.o_free[WIDE ? i : 0]);
             if (tid == 0 && g.t0 == 0 && !whole)
                 tp.cuts[cta] = make_int4(g.b, g.h, g.tok0 | min(g.s.n - g.tok0, tok_per) << 16, g.last_cta);
             end(seg);
@@ -718,6 +724,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
             const uint64_t qd = swz128_desc(smem_u32(qtile), 16, 1024), kd = swz128_desc(smem_u32(ring), 16, 1024);
             const uint64_t vd = swz128_desc(smem_u32(ring), BLOCK, 1024);
             uint32_t item = 0, count[2] = {0, 0};                 // ring items before the segment, tiles of each group
+            uint32_t outputs[2] = {0, 0};                         // segments in which each output was written before
             auto scores = [&](int i, uint32_t at) {
                 const uint64_t a = qd + (uint64_t)((WIDE ? i : 0) * NB * BLOCK >> 4);
                 const uint64_t k0 = kd + (uint64_t)(at % NS * (kv_bytes<D>() >> 4));
@@ -779,7 +786,11 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                         const int i = WIDE ? x : j & 1;
                         if (!ok || (WIDE && x >= groups)) continue;
                         ok = wait_one(&sh.p_full[i], count[i] & 1);      // the weights, this value tile and the next key tile
-                        if (ok && j < LEAD && seg > 0) ok = wait_one(&sh.o_free, (seg - 1) & 1);
+                        if (ok && j < LEAD) {
+                            const int o = WIDE ? i : 0;
+                            ok = outputs[o] == 0 || wait_one(&sh.o_free[o], (outputs[o] - 1) & 1);
+                            if (WIDE) ++outputs[o];
+                        }
                         if (!ok) continue;
                         tc_fence_after();
                         output(i, vt, j >= LEAD);
@@ -800,6 +811,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                     }
                 }
                 item += 2 * n;
+                if (!WIDE) ++outputs[0];
             }
             // nothing of this CTA is under way when its tensor memory goes back
             tc_commit(&sh.drained);

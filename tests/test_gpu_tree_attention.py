@@ -16,6 +16,17 @@ def _lib():
     build.build()
 
 
+@pytest.fixture(params=["rule", "whole", "cut"], autouse=True)
+def _form(request, monkeypatch):
+    """The form that the sizes choose, and the two of the tree kernel, which small calls would not reach."""
+    if request.param == "rule":
+        monkeypatch.delenv("QASA_TREE_FORM", raising=False)
+    elif "f32" in request.node.name or "mask" in request.node.name or "parents" in request.node.name:
+        pytest.skip("has one form")
+    else:
+        monkeypatch.setenv("QASA_TREE_FORM", request.param)
+
+
 def _qasa():
     from query_aware_sparse_append_gb300 import binding
     return binding
