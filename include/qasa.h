@@ -238,9 +238,10 @@ qasa_status qasa_kv_append_positioned(const qasa_kv_cache *cache, const qasa_rot
  * every page from the start's on that then holds tokens (of the start's page only if it
  * does) is taken anew from all its tokens, so that tokens given up leave it.  E4M3: amax
  * of such a page becomes the largest of what it was and the |value| (code * s, fp32) of
- * the tokens that come from other pages; where it grows the page's codes are
- * re-quantised as by an append, and tokens from other pages are stored as
- * code(code * s_src / s_new).  Slots behind the last token are left as they were.
+ * the tokens that come from other pages; where it grows the page's codes become
+ * code(code * s_old / s_new), and tokens from other pages are stored as
+ * code(code * s_src / s_new); a quotient within 2^-22 of the border between two codes gets
+ * the even one, so that no rounding on the way decides.  Slots behind the last token are left as they were.
  * A token whose page has a bad block-table entry is not moved (QASA_DEVERR_PAGE_ID): its
  * new slot, if that has a page, keeps what it held.  Pages that the call writes must belong
  * to one sequence only.

@@ -413,9 +413,12 @@ def _positions(positions: torch.Tensor, axes, B: int, T: int, half: int, index: 
     if not 1 <= num <= 3:
         raise ValueError("positions must have one to three axes")
     if axes is not None:
-        if len(axes) != half or not all(0 <= a < num for a in axes):
+        try:
+            axes = bytes(axes)          # bytes are taken as they are
+        except ValueError:
+            axes = b""
+        if len(axes) != half or max(axes) >= num:
             raise ValueError("pair_axes must hold an axis of positions for each of the table's pairs")
-        axes = bytes(axes)
     return _Positions(positions.data_ptr(), positions.stride(0) if len(shape) == 3 else 0,
                       positions.stride(-2) if shape[-2] > 1 else 0, num, axes)
 
@@ -438,9 +441,9 @@ def kv_append_positioned(cache: PagedKVCache, block_table: torch.Tensor, seq_len
                            (positions, pair_axes), status, stream)
 
 
-def pair_sections(sections: Sequence[int]) -> list:
+def pair_sections(sections: Sequence[int]) -> bytes:
     """pair_axes of channel pairs in one span per axis, of these numbers of pairs."""
-    return [axis for axis, n in enumerate(sections) for _ in range(n)]
+    return bytes(axis for axis, n in enumerate(sections) for _ in range(n))
 
 
 def kv_keep_tokens(cache: PagedKVCache, block_table: torch.Tensor, seq_lens: torch.Tensor, starts: torch.Tensor,

@@ -30,7 +30,7 @@
 // turning by the position on its own axis (a tree of drafted tokens, whose siblings
 // share a position; image tokens with a time, a height and a width).  Slots still
 // follow the lengths.  A lane's pairs are EPC neighbours of the table row, mostly of
-// one axis, so it reads the rows of the axes that it has and picks.
+// one axis: four that are come with one load, others one by one.
 #include "page_rows.cuh"
 #include "qasa_launch.h"
 
@@ -106,21 +106,25 @@ __device__ __forceinline__ void load_angles(Angles<EPC> &a, const RotatedParams 
 template <int EPC>
 __device__ __forceinline__ void load_angles(Angles<EPC> &out, const RotatedParams &p, const Given &g, const LanePair &l) {
     if (!l.turns) return;
+    auto row = [&](uint32_t axis) {
+        return p.table + (size_t)(axis == 0 ? g.at[0] : axis == 1 ? g.at[1] : g.at[2]) * p.rot + l.angle;
+    };
 #pragma unroll
-    for (int a = 0; a < 3; ++a) {
-        // the lane's pairs on this axis: bit 2 e for pair e
-        const uint32_t lo = l.axes, hi = l.axes >> 1, ones = 0x55555555u & ((1u << (2 * EPC)) - 1u);
-        const uint32_t mine = (a == 0 ? ~lo & ~hi : a == 1 ? lo & ~hi : ~lo & hi) & ones;
-        if (!mine) continue;
-        const float *row = p.table + (size_t)g.at[a] * p.rot + l.angle;
+    for (int e = 0; e < EPC; e += 4) {
+        const uint32_t four = l.axes >> (2 * e) & 0xffu, axis = four & 3u;
+        if (four == axis * 0x55u) {               // four pairs of one axis
+            const float *at = row(axis) + e;
+            const float4 c = __ldg(reinterpret_cast<const float4 *>(at));
+            const float4 s = __ldg(reinterpret_cast<const float4 *>(at + p.rot / 2));
+            out.c[e] = c.x; out.c[e + 1] = c.y; out.c[e + 2] = c.z; out.c[e + 3] = c.w;
+            out.s[e] = s.x; out.s[e + 1] = s.y; out.s[e + 2] = s.z; out.s[e + 3] = s.w;
+        } else {
 #pragma unroll
-        for (int e = 0; e < EPC; e += 4) {
-            const float4 c = __ldg(reinterpret_cast<const float4 *>(row + e));
-            const float4 s = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + e));
-            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (mine >> (2 * (e + k)) & 1u) { out.c[e + k] = cs[k]; out.s[e + k] = sn[k]; }
+            for (int k = 0; k < 4; ++k) {
+                const float *at = row(four >> (2 * k) & 3u) + e + k;
+                out.c[e + k] = __ldg(at);
+                out.s[e + k] = __ldg(at + p.rot / 2);
+            }
         }
     }
 }
@@ -476,7 +480,7 @@ __device__ __forceinline__ void append_kv_fp8(const RotatedParams &p, int b, int
 
 // T: the type of q and of the new rows; FP8: E4M3 pools.
 template <typename T, int D, bool FP8, bool INTER, bool GIVEN>
-__global__ void __launch_bounds__(32 * kWarps, 5) append_rotated_kernel(RotatedParams p) {
+__global__ void __launch_bounds__(32 * kWarps, FP8 && GIVEN ? 4 : 5) append_rotated_kernel(RotatedParams p) {
     const int b = blockIdx.y, x = blockIdx.x;
     if (x < p.kv_blocks) {
         const int per_page = (2 * p.Hkv + kWarps - 1) / kWarps;

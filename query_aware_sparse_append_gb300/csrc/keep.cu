@@ -34,19 +34,28 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Length of the list that holds: `n` entries, or up to the first that does not ascend or
-// lies at or past `end` (positions counted from the start).  All threads of the CTA.
-__device__ __forceinline__ int good_entries(const int32_t *keep, int n, int end) {
+// lies at or past `end` (positions counted from the start).  All threads of the cluster,
+// whose CTAs look at a part of the list each.
+__device__ __forceinline__ int good_entries(const int32_t *keep, int n, int end, int rank, int cluster) {
     __shared__ int bad;
     if (threadIdx.x == 0) bad = n;
     __syncthreads();
     int mine = n;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int at = keep[i], before = i ? keep[i - 1] : -1;
-        if (at <= before || at >= end) { mine = i; break; }
+#pragma unroll 4
+    for (int i = rank * blockDim.x + threadIdx.x; i < n; i += cluster * blockDim.x) {
+        const int at = __ldg(keep + i), before = i ? __ldg(keep + i - 1) : -1;
+        if (at <= before || at >= end) mine = min(mine, i);
     }
     if (mine < n) atomicMin(&bad, mine);
-    __syncthreads();
-    return bad;
+    if (cluster == 1) {
+        __syncthreads();
+        return bad;
+    }
+    cluster_sync();
+    int least = n;
+    for (int k = 0; k < cluster; ++k) least = min(least, ld_cluster_s32(map_rank(&bad, k)));
+    cluster_sync();                                // nobody leaves while its word is read
+    return least;
 }
 
 // T: type of the pool's elements as chunks go (E4M3: codes).
@@ -68,7 +77,7 @@ __global__ void __launch_bounds__(kMostWarps * 32) keep_kernel(KeepParams p) {
     if (start < 0 || start > L) { err |= QASA_DEVERR_SEQ_LEN; start = start < 0 ? 0 : L; }
     if (n < 0 || n > p.M) { err |= QASA_DEVERR_APPEND; n = n < 0 ? 0 : p.M; }
     const int32_t *keep = p.keep + (size_t)b * p.M;
-    const int good = good_entries(keep, n, L - start);
+    const int good = good_entries(keep, n, L - start, rank, cluster);
     if (good < n) { err |= QASA_DEVERR_KEEP; n = good; }
     if (first) {
         if (err && p.status) atomicOr(p.status, err);
@@ -81,43 +90,49 @@ __global__ void __launch_bounds__(kMostWarps * 32) keep_kernel(KeepParams p) {
     unsigned char *pool = static_cast<unsigned char *>(which ? p.v_pool : p.k_pool);
     unsigned char *mine = smem + (size_t)warp * p.P * ROWB;
 
-    // every CTA of the cluster goes through the same rounds
-    for (int round = 0; round < pages; round += per_round) {
-        const int at = round + rank * warps + warp;
-        int rows = 0, src = -1, dst = -1, phys = -1;           // src, dst: pool rows of this lane's slot
-        bool other = false;                                    // it comes from another page
-        float s_src = 0.f, old = 0.f;
-        if (at < pages) {
-            const int page = page0 + at, base = page * p.P;
-            rows = min(p.P, end - base);
-            phys = table[page];
-            const bool bad = phys < 0 || phys >= p.num_phys;
-            if (bad) {
-                phys = -1;
-                if (lane == 0 && p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
-            }
-            if (lane < rows && !bad) {
-                const int pos = base + lane;
-                dst = (phys * p.Hkv + h) * p.P + lane;
-                src = dst;
-                if (pos >= start) {
-                    const int from = start + keep[pos - start], fp = from / p.P;
-                    if (fp != page) {
-                        const int sp = table[fp];
-                        other = sp >= 0 && sp < p.num_phys;
-                        if (!other && p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
-                        if (other) {
-                            src = (sp * p.Hkv + h) * p.P + from % p.P;
-                            if constexpr (FP8) s_src = fp8_scale(p.scales[((size_t)sp * p.Hkv + h) * 4 + which]);
-                        }
-                    } else {
-                        src = dst - lane + from % p.P;
-                    }
+    // A warp's page of a round: its rows and where this lane's slot comes from and goes to.
+    struct Place {
+        int rows, src, dst, phys;                              // src, dst: pool rows; phys < 0: no page
+        bool other;                                            // it comes from another page,
+        float from, old;                                       // E4M3: of this amax; the page's own
+    };
+    auto look_up = [&](int at) {
+        Place x{0, -1, -1, -1, false, 0.f, 0.f};
+        if (at >= pages) return x;
+        const int page = page0 + at, base = page * p.P, pos = base + lane;
+        const int from = pos >= start && pos < end && lane < p.P ? start + __ldg(keep + pos - start) : pos;
+        const int phys = table[page];
+        if (phys < 0 || phys >= p.num_phys) {
+            if (lane == 0 && p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
+            return x;
+        }
+        x.phys = phys;
+        x.rows = min(p.P, end - base);
+        if (lane < x.rows) {
+            x.dst = x.src = (phys * p.Hkv + h) * p.P + lane;
+            const int fp = from / p.P;
+            if (fp == page) {
+                x.src = x.dst - lane + from % p.P;
+            } else {
+                const int sp = table[fp];
+                x.other = sp >= 0 && sp < p.num_phys;
+                if (!x.other && p.status) atomicOr(p.status, QASA_DEVERR_PAGE_ID);
+                if (x.other) {
+                    x.src = (sp * p.Hkv + h) * p.P + from % p.P;
+                    if constexpr (FP8) x.from = p.scales[((size_t)sp * p.Hkv + h) * 4 + which];
                 }
             }
-            if (FP8 && phys >= 0) old = p.scales[((size_t)phys * p.Hkv + h) * 4 + which];
-            if (phys < 0) rows = 0;
         }
+        if constexpr (FP8) x.old = p.scales[((size_t)phys * p.Hkv + h) * 4 + which];
+        return x;
+    };
+    // every CTA of the cluster goes through the same rounds
+    Place next = look_up(rank * warps + warp);
+    for (int round = 0; round < pages; round += per_round) {
+        const int at = round + rank * warps + warp;
+        const int rows = next.rows, src = next.src, dst = next.dst, phys = next.phys;
+        const bool other = next.other;
+        const float amax_src = next.from, old = next.old;
         const int need = FP8 || !which ? 0 : max(start - (page0 + at) * p.P, 0);   // V: earlier rows stay as they are
         // all rows of the page under way, then everybody's
         for (int x0 = 0; x0 < rows * (ROWB / 16); x0 += 32) {
@@ -125,6 +140,8 @@ __global__ void __launch_bounds__(kMostWarps * 32) keep_kernel(KeepParams p) {
             const int from = __shfl_sync(0xffffffffu, src, r & 31);
             if (r >= need && r < rows) copy_async16(smem_u32(mine + r * ROWB + c * 16), pool + (size_t)from * ROWB + c * 16);
         }
+        // the next round's places meanwhile; its scales are those of pages that no round before has written
+        next = look_up(at + per_round);
         copy_async_wait();
         if (cluster > 1) cluster_sync(); else __syncthreads();
         __syncwarp();
@@ -134,7 +151,7 @@ __global__ void __launch_bounds__(kMostWarps * 32) keep_kernel(KeepParams p) {
             float top = 0.f;
             for (int r0 = 0; r0 < rows; r0 += RPP) {           // the largest |value| that comes from other pages
                 const int r = r0 + lane / LPR;
-                const float s = __shfl_sync(0xffffffffu, s_src, r & 31);
+                const float s = fp8_scale(__shfl_sync(0xffffffffu, amax_src, r & 31));
                 const bool comes = __shfl_sync(0xffffffffu, (int)other, r & 31) != 0 && r < rows;
                 if (comes) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(mine + r * ROWB + c * 16);
@@ -147,29 +164,20 @@ __global__ void __launch_bounds__(kMostWarps * 32) keep_kernel(KeepParams p) {
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const float amax = fmaxf(old, top);
-            const float s_old = fp8_scale(old), s_new = fp8_scale(amax), inv = 1.f / s_new;
             const bool grown = amax > old;
             Box<__half> box;
             box.clear();
             for (int r0 = 0; r0 < rows; r0 += RPP) {
                 const int r = r0 + lane / LPR;
-                const float s = __shfl_sync(0xffffffffu, s_src, r & 31);
+                const float a = __shfl_sync(0xffffffffu, amax_src, r & 31);
                 const bool comes = __shfl_sync(0xffffffffu, (int)other, r & 31) != 0;
                 const int from = __shfl_sync(0xffffffffu, src, r & 31), to = __shfl_sync(0xffffffffu, dst, r & 31);
                 if (r >= rows) continue;
                 uint4 w = *reinterpret_cast<const uint4 *>(mine + r * ROWB + c * 16);
                 if (comes || grown) {
-                    const float by = comes ? s : s_old;
-                    uint2 half[2] = {make_uint2(w.x, w.y), make_uint2(w.z, w.w)};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float v[8];
-                        codes_to_f(half[k], v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], by);
-                        half[k] = quantise8(v, s_new, inv);
-                    }
-                    w = make_uint4(half[0].x, half[0].y, half[1].x, half[1].y);
+                    const float was = comes ? a : old, by = __fdiv_rn(was, amax);
+                    const uint2 lo = recode8(make_uint2(w.x, w.y), by, was, amax), hi = recode8(make_uint2(w.z, w.w), by, was, amax);
+                    w = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
                 if (comes || grown || from != to) *reinterpret_cast<uint4 *>(pool + (size_t)to * ROWB + c * 16) = w;
                 if (!which) box.fold(codes_to_halves(make_uint2(w.x, w.y)), codes_to_halves(make_uint2(w.z, w.w)));

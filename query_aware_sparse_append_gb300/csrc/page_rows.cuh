@@ -94,6 +94,50 @@ __device__ __forceinline__ uint2 quantise8(const float *y, float s, float inv) {
     return make_uint2(w[0], w[1]);
 }
 
+// Codes under a page's scale of values that are codes under another one's: c a / a_new of
+// code values c and the two pages' amax (the 448 of both scales cancels), eight at a time.
+// Such quotients often lie on the border of two codes exactly, as a_new is itself some
+// code times a scale; its two fp32 roundings, 2^-23 of it, must not decide there, so within
+// 2^-22 of a border the even code is taken.  Out of line, in 64 bits: only quotients that
+// are near a border in fp32 come here.
+static __device__ __noinline__ uint2 recode8_near(float4 a, float4 b, float amax, float amax_new) {
+    const float c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const double ratio = amax_new > 0.f ? (double)amax / (double)amax_new : 0.0;
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const double q = c[e] * ratio;
+        const uint32_t in = code2((float)(q * (1.0 - 0x1p-22)), 0.f) & 0xffu, out = code2((float)(q * (1.0 + 0x1p-22)), 0.f) & 0xffu;
+        w[e >> 2] |= (out & 1u ? in : out) << (8 * (e & 3));       // the same code twice, or neighbours, of which one is even
+    }
+    return make_uint2(w[0], w[1]);
+}
+// `by` = amax / amax_new in fp32, or infinite or NaN where that is no number.  Its product with a
+// code value is within 2^-23 of the quotient: where products scaled by 1 - 2^-21 and 1 + 2^-21
+// have the same code, no border is within 2^-22 of it.
+__device__ __forceinline__ uint2 recode8(const uint2 &codes, float by, float amax, float amax_new) {
+    float c[8];
+    codes_to_f(codes, c);
+    uint32_t w[2] = {0u, 0u};
+    bool same = by < INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float a = c[e] * by, b = c[e + 1] * by;
+        const uint32_t in = code2(a * (1.f - 0x1p-21f), b * (1.f - 0x1p-21f));
+        const uint32_t out = code2(a * (1.f + 0x1p-21f), b * (1.f + 0x1p-21f));
+        same = same && in == out;
+        w[e >> 2] |= out << (8 * (e & 2));
+    }
+    if (!same) {
+        const uint2 x = recode8_near(make_float4(c[0], c[1], c[2], c[3]), make_float4(c[4], c[5], c[6], c[7]), amax, amax_new);
+        w[0] = x.x;
+        w[1] = x.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) w[k] &= ((w[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | 0x7f7f7f7fu;   // zero is +0
+    return make_uint2(w[0], w[1]);
+}
+
 // Eight codes as halves, exactly, and back (halves that are codes' values).
 __device__ __forceinline__ uint4 codes_to_halves(const uint2 &w) {
     return make_uint4(e4m3x2_to_h2(w.x), e4m3x2_to_h2(w.x >> 16), e4m3x2_to_h2(w.y), e4m3x2_to_h2(w.y >> 16));

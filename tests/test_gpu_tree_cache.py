@@ -195,11 +195,13 @@ def _random_kept(total, n, g):
 
 
 def _compare(now, want, dtype):
-    """Everything equal, but that an E4M3 code may be the neighbouring one where both are as far from the quotient.
+    """Everything equal, but that an E4M3 code may be the neighbouring one where both are nearly as far from the quotient.
 
-    The library's quotient code * s_src / s_new has four fp32 roundings (two scales, product, division), 2^-24 each
-    and 2^-23 of amax in s_new: less than 2^-21 in all, so a code other than the nearest one of the 64-bit quotient lies
-    on the other side of a border that is within 2^-21 of it, and the two distances differ by less than 2^-20 of it.
+    The library takes the even code where its quotient code * amax_src / amax lies within 2^-22 of a border between two
+    codes, else the nearest.  Its amax has two fp32 roundings that the 64-bit one has not (the scale and a product), 2^-24
+    each, the quotient's ends are rounded to fp32, 2^-24.  So a code other than the nearest one of the 64-bit quotient y
+    lies on the other side of a border that is within (2^-22 + 2^-23 + 2^-24) y of y, less than 2^-21 y, and its distance
+    from y exceeds the nearest one's by less than twice that.
     That is no rare event: amax is itself some code * s_src, so that quotients are 448 x / c of two codes x and c, which
     fall on borders exactly for some x, and then for every x of the page."""
     touched, quotients = want.pop("touched"), want.pop("quotients")

@@ -161,4 +161,4 @@ def test_binding_checks_tensors(lib):
             lib._positions(pos, axes, 1, 2, 32, -1)
     got = lib._positions(pos.view(1, 1, 2).expand(3, 1, 2), lib.pair_sections([8, 12, 12]), 5, 2, 32, -1)
     assert (got.axis_stride, got.batch_stride, got.num_axes) == (0, 0, 3)
-    assert lib.pair_sections([1, 2, 1]) == [0, 1, 1, 2]
+    assert list(lib.pair_sections([1, 2, 1])) == [0, 1, 1, 2]
