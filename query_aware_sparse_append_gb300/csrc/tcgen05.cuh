@@ -91,8 +91,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
                  : "memory");
 }
 
-// Waits for the loads of 32 registers, whose uses cannot move before it.
+// Waits for the loads of 32 (16) registers, whose uses cannot move before it.
 #define QASA_INOUT(x) "+r"(x)
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QASA_R8(QASA_INOUT, 0), QASA_R8(QASA_INOUT, 8) :: "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t *r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : QASA_R8(QASA_INOUT, 0), QASA_R8(QASA_INOUT, 8), QASA_R8(QASA_INOUT, 16), QASA_R8(QASA_INOUT, 24)

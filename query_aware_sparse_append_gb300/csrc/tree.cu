@@ -525,7 +525,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(oa + c, o);
-                            tmem_wait_ld();
+                            tmem_wait_ld16(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                             tmem_st16(oa + c, o);
@@ -621,7 +621,7 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                             for (int before = 0; before < c; ++before) {
                                 uint32_t y[16];
                                 tmem_ld16(sa + 16 * before, y);
-                                tmem_wait_ld();
+                                tmem_wait_ld16(y);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
                                     const float2 v = unpack2<T>(y[e]);
