@@ -219,6 +219,66 @@ def test_bad_lengths_are_clamped_and_reported(T):
     assert bool((out[1] == 9).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "e4m3"])
+@pytest.mark.parametrize("T", [6, 40, 150])
+def test_more_drafted_tokens_than_the_sequence_has(dtype, T):
+    # those before position 0 do not exist: nobody sees them, and their own queries see what their rows show
+    c = R.Paged(dtype, [3, T + 20, T - 1], 2, 64, 16, seed=55)
+    q = _queries(c, T, 8)
+    rows, mask = _trees(c, T, [T] * 3)
+    out = _run(c, q, [T] * 3, rows, mask, None, 0, T)
+    _check(c, q, out, [T] * 3, rows, None, 0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "e4m3"])
+def test_more_sequences_than_threads(dtype):
+    B, T = 900, 3
+    lens = [T + 7 * (b % 13) + (90 if b % 97 == 5 else 0) for b in range(B)]
+    n = [b % (T + 1) for b in range(B)]
+    c = R.Paged(dtype, lens, 1, 64, 16, seed=56)
+    q = _queries(c, T, 2)
+    rows, mask = _trees(c, T, n)
+    out = _run(c, q, n, rows, mask, 30, 2, T)
+    _check(c, q, out, n, rows, 30, 2)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "e4m3"])
+@pytest.mark.parametrize("T,group", [(10, 8), (60, 4)])
+def test_waits_with_a_short_limit_end_and_leave_rows_right_or_as_they_were(dtype, T, group, monkeypatch):
+    qasa = _qasa()
+    c = R.Paged(dtype, [1600, 300, T], 2, 128, 16, seed=57)
+    q = _queries(c, T, 2 * group)
+    n = [T] * 3
+    rows, mask = _trees(c, T, n)
+    clean = _run(c, q, n, rows, mask, None, 0, T)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("QASA_WAIT_LIMIT_NS", "1000")
+    out = torch.full_like(q, 9.0)
+    qasa.tree_attention(c.library(), q, c.table, c.seq_lens, mask, out=out, status=status)
+    torch.cuda.synchronize()
+    assert int(status) in (0, 0x8), hex(int(status))
+    same = (out == clean).all(-1) | (out == 9.0).all(-1)
+    assert bool(same.all())
+    if int(status) == 0:
+        assert torch.equal(out, clean)
+    monkeypatch.delenv("QASA_WAIT_LIMIT_NS")
+    out = _run(c, q, n, rows, mask, None, 0, T)
+    assert torch.equal(out, clean)
+
+
+def test_empty_calls():
+    qasa = _qasa()
+    c = R.Paged("f16", [40], 2, 64, 16, seed=58)
+    q = _queries(c, 4, 8)
+    mask = torch.zeros((1, 4, 1), dtype=torch.int32, device="cuda")
+    got = qasa.tree_attention(c.library(), q[:, :0], c.table, c.seq_lens, mask[:, :0, :0])
+    assert got.shape == (1, 0, 8, 64)
+    got = qasa.tree_attention(c.library(), q[:0], c.table[:0], c.seq_lens[:0], mask)
+    assert got.shape == (0, 4, 8, 64)
+    m, d = qasa.tree_masks(torch.zeros((2, 0), dtype=torch.int32, device="cuda"))
+    assert m.shape == (2, 0, 0) and d.shape == (2, 0)
+
+
 @pytest.mark.parametrize("dtype,T,group", [("f16", 2, 4), ("f16", 24, 8), ("f16", 64, 8), ("e4m3", 24, 8), ("f32", 6, 2)])
 def test_nan_and_infinite_queries_reach_their_own_rows_alone(dtype, T, group):
     c = R.Paged(dtype, [500 + T, T + 33], 2, 128, 16, seed=49)
