@@ -314,6 +314,23 @@ def test_keep_repeats_and_replays_on_another_stream(dtype):
         assert all(X.same(a[name], b[name]) for name in a)
 
 
+@pytest.mark.parametrize("power", [-90, 90])
+def test_codes_do_not_depend_on_the_size_of_the_scales(power):
+    # scales times a power of two change no quotient and round alike: the same codes
+    qasa = _qasa()
+    g = torch.Generator(device="cpu").manual_seed(78)
+    lens, starts = [300, 800, 90], [3, 160, 0]
+    keep = _ints([_random_kept(L - s, 80, g) for L, s in zip(lens, starts)])
+    a, b = (R.Paged("e4m3", lens, 3, 128, 16, seed=79, amax_spread=1.0) for _ in range(2))
+    b.scales *= 2.0 ** power
+    for c in (a, b):
+        qasa.kv_keep_tokens(c.library(), c.table, c.seq_lens, _ints(starts), keep)
+    torch.cuda.synchronize()
+    x, y = X.stored(a), X.stored(b)
+    y["scales"] *= 2.0 ** -power
+    assert all(X.same(x[name], y[name]) for name in x)
+
+
 # -------------------------------------------------------------------- copies and forks
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16", "e4m3"])
