@@ -61,7 +61,7 @@ namespace {
 constexpr int kRows = 128;            // rows of a row tile
 constexpr int kKeys = 128;            // tokens of a key tile
 constexpr int kUnitCost = 2;          // tiles that a unit's beginning and end are worth
-constexpr int kScaleRing = 8;         // key tiles whose E4M3 scales are kept
+constexpr int kScaleRing = 16;        // key tiles whose E4M3 scales are kept (a power of two)
 constexpr int kSegments = 4;          // segments told ahead
 constexpr float kLeastShare = -60.f;  // log2 of the least share of the largest value scale that a weight carries
 constexpr float kGivenUp = 3e38f;     // maximum that a CTA reports for rows that it gave up
@@ -353,6 +353,9 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
     constexpr int NS = kStages<D, FP8, WIDE>, NC = kCodeStages<D, FP8, WIDE>;
     constexpr int NQ = WIDE ? 2 : 1;                  // row tiles of a unit
     constexpr int LEAD = WIDE ? 1 : 2;                // key tiles ahead of the value tiles in the ring
+    // The scales of a tile are written when those copies alone are waited for that lie NS + NC items before its
+    // keys: with two items to a tile, a softmax may still read the scales of a tile that much further back.
+    static_assert(!FP8 || (NS + NC + 1) / 2 + LEAD <= kScaleRing, "a tile's scales stay until its softmax is done");
     constexpr int ROWS = NQ * kRows;
     constexpr int THREADS = tree_threads<FP8>();
     constexpr uint32_t S_COL[2] = {0, 128}, O_COL[2] = {256, 256 + D}, TMEM = 512;
