@@ -39,6 +39,13 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Magnitudes of four codes, which are in the order of their values; a NaN's, 0x7f, counts as
+// zero: it takes no finite code beside it out of the largest one.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
+    w &= 0x7f7f7f7fu;
+    return w & ~(((w + 0x01010101u) >> 7 & 0x01010101u) * 0xffu);
+}
+
 // Length of the list that holds: `n` entries, or up to the first that does not ascend or
 // lies at or past `end` (positions counted from the start).  All threads of the cluster,
 // whose CTAs look at a part of the list each.
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kMostWarps * 32) keep_kernel(KeepParams p) {
                 const bool comes = __shfl_sync(0xffffffffu, (int)other, r & 31) != 0 && r < rows;
                 if (comes) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(mine + r * ROWB + c * 16);
-                    uint32_t m = __vmaxu4(__vmaxu4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu), __vmaxu4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu));
+                    uint32_t m = __vmaxu4(__vmaxu4(magnitudes(w.x), magnitudes(w.y)), __vmaxu4(magnitudes(w.z), magnitudes(w.w)));
                     m = __vmaxu4(m, m >> 16);
                     m = max(m & 0xffu, m >> 8 & 0xffu);
                     top = fmaxf(top, __fmul_rn(e4m3_to_f(m), s));
