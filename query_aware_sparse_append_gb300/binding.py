@@ -414,8 +414,8 @@ def _positions(positions: torch.Tensor, axes, B: int, T: int, half: int, index: 
         raise ValueError("positions must have one to three axes")
     if axes is not None:
         try:
-            axes = bytes(axes)          # bytes are taken as they are
-        except ValueError:
+            axes = axes if isinstance(axes, bytes) else bytes(list(axes))   # of a number, bytes() would make zeros
+        except (TypeError, ValueError):
             axes = b""
         if len(axes) != half or max(axes) >= num:
             raise ValueError("pair_axes must hold an axis of positions for each of the table's pairs")
