@@ -205,7 +205,12 @@ qasa_status qasa_kv_append_rotated(const qasa_kv_cache *cache, const qasa_rotati
  *     data[pair_axes[i] * axis_stride + b * batch_stride + t]
  * Everything else is as in qasa_kv_append_rotated: token t goes to the slot of position
  * seq_lens[b] + t.  A token with a position outside [0, max_positions) on any axis is
- * skipped, q included, its slot left as it was, and sets QASA_DEVERR_POSITION.
+ * skipped, q included, its slot left as it was, and sets QASA_DEVERR_POSITION.  Its slot
+ * then holds no token: a caller that sees the bit makes the call again, from the same
+ * lengths and with positions that the table has, before any other call is given lengths
+ * that pass the slot.  (A page of which a call stores nothing keeps the box and the scales
+ * that it had; where slot 0 is among the skipped ones these are of what the page held for
+ * somebody else, and a later append behind slot 0 would take them for the sequence's own.)
  */
 typedef struct {
     const int32_t *data;       /* device */

@@ -431,7 +431,8 @@ def kv_append_positioned(cache: PagedKVCache, block_table: torch.Tensor, seq_len
     """kv_append_rotated with the positions of the new tokens given, int32 [B, T] or [axes, B, T] (B or 1, up to
     three axes): a tree's tokens turn by their depth behind the context, image tokens by their time, height and
     width.  pair_axes: the axis of each of the table's channel pairs (None: the first); see pair_sections.  The
-    tokens still go to the slots after seq_lens."""
+    tokens still go to the slots after seq_lens.  Tokens with a position that the table has not are skipped (status
+    0x40): call again, from the same seq_lens, before their slots count as filled."""
     index = cache.device_index
     if index >= 0 and _get_device() != index:
         with torch.cuda.device(index):
