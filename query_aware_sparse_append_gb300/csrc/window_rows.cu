@@ -354,12 +354,15 @@ __global__ void __launch_bounds__(W * 32, ROWS == 8 ? 4 : 3) window_rows_kernel(
 #pragma unroll
                 for (int x = 0; x < NH; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                    {
-                        const int j = tok0[t] + 8 * (e >> 1) + g4;
-                        const bool seen = TREE ? tree_sees(mask[x][e & 1], pos[x][e & 1], j, s.first, s.len, p.window, p.sinks)
-                                               : sees(pos[x][e & 1], j, p.window, p.sinks);
-                        if (!good[t] || !seen) sc[t][x][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (TREE) {
+                            if (!good[t] || !tree_sees(mask[x][e & 1], pos[x][e & 1], tok0[t] + 8 * (e >> 1) + g4, s.first, s.len,
+                                                       p.window, p.sinks))
+                                sc[t][x][e] = -INFINITY;
+                        } else {
+                            if (!good[t] || !sees(pos[x][e & 1], tok0[t] + 8 * (e >> 1) + g4, p.window, p.sinks))
+                                sc[t][x][e] = -INFINITY;
+                        }
                     }
         }
         if constexpr (FP8) {
