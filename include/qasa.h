@@ -464,7 +464,10 @@ qasa_status qasa_window_attention(const qasa_kv_cache *cache, const void *q, int
  * tiles of max_pages_per_seq pages (two more counted) times the blocks of 128 (256) query
  * rows of a KV head up to 2^31 - 1.  Precision, scale, bad pages, NaN
  * queries and QASA_DEVERR_TIMEOUT as in qasa_window_attention; a query that sees
- * nothing gets zeros.  Keys and values must be finite of the context's tokens that a
+ * nothing gets zeros.  E4M3: a weight is rounded together with its page's value scale, as a
+ * share of the largest such scale among the row block's keys: half a step, relative, down to
+ * 2^-21 of the row's largest weight, and 2^-32 of that weight where the two together are less.
+ * Keys and values must be finite of the context's tokens that a
  * query at depth 0 sees and of the drafted tokens that some query sees; other slots
  * may hold anything.
  */

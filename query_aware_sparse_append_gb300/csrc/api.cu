@@ -582,6 +582,13 @@ const char *tree_form() {
 // kernel, a tile 10.5 (13) ns on the tree kernel.  The few-rows kernel's clusters of eight do
 // not fill the device with few units: 32000 tokens of 8 heads take 55 to 66 us for up to 16
 // rows there, 38 us here.
+//
+// The tiles counted are those of the block table, not of a window, so that a call's form and
+// workspace follow from its sizes alone.  With a window of 1024 over tables of 4000 tokens (the same
+// over 32000, but for one sequence) the times per call of rule | few | cut | whole units are, f16 and
+// (E4M3): 16 x 24 tokens 33|65|33|31 (38|68|38|36), 64 x 8 54|83|54|51 (71|93|71|52), 64 x 2 33|34|52|49
+// (34|33|70|51), 1 x 64 23|21|23|32 (25|23|25|38), 4 x 16 21|21|22|27 (22|23|22|27): the rule is at
+// most 10 % behind the best, but for many E4M3 units of some ten visible tiles (71 and 52).
 TreePlan tree_plan(const qasa_kv_cache *c, int batch, int num_q_heads, int T, int max_pages) {
     TreePlan r = {};
     const int G = num_q_heads / c->num_kv_heads, per = 128 / G;

@@ -43,8 +43,12 @@
 // tokens over 500 to 4000, f16, 35 us (2.2 TB/s: 13 us are the start, the first tile and the
 // join); 64 tokens over 32704, bf16, 48 us (2.8 TB/s, 0.71 PFLOP/s); 64 x 32 tokens over 8160,
 // E4M3, 320 us (0.86 PFLOP/s).  One row tile per KV head (64 x 16 tokens over 8000, f16) streams
-// at 5.6 TB/s.  In the middle of a call a pair of row tiles takes 3600 cycles for 128 tokens:
-// 1900 for a group's softmax, 1600 until its next scores, the two groups in turn.
+// at 5.6 TB/s.  In the middle of a call a pair of row tiles takes 3450 cycles for 128 tokens of
+// 16-bit pages: 1650 for a group's softmax, 1800 until its next scores, the two groups in turn.
+// E4M3: 4600 to 5050, 2500 and 2150 to 2500 (the softmax looks up scales and shares, and the
+// converting warps, busy 45 % of the time, share the issue slots and shared memory).  The 108 tiles of
+// a CTA of the large case are 510 to 550 thousand cycles, its start 15, each of its one or two ends of
+// units 13: 600 thousand, 308 us at the 1.96 GHz that it runs at, and the join.
 //
 // Measured and slower: the whole tile's softmax unrolled (its 800 instructions are fetched by
 // all SMs at once in every launch, and the two groups then meet: E4M3 400 us) or 64 tokens at
@@ -620,7 +624,9 @@ tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                                     w.x = exp2_fast(w.x);
                                     w.y = exp2_fast(w.y);
                                     sum[e / 2 & 1] = add2(sum[e / 2 & 1], w);
-                                    // weights in the values' 16-bit type: half a step each, while the sum keeps fp32
+                                    // weights in the values' 16-bit type, which both operands of the product share: half a
+                                    // step each, while the sum keeps fp32 (what the rounding takes off would be a second
+                                    // product, and columns that tensor memory has not)
                                     w16[(h * 16 + e) / 2] = mma16816<T>::pack2(w.x, w.y);
                                 }
                                 sum[0] = add2(sum[0], sum[1]);
